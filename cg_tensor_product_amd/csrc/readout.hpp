@@ -1,0 +1,54 @@
+// Launchers of the readout operators (group_norm.hip, dropout.hip, cross_attn_*.hip),
+// called by capi_readout.cpp with checked arguments.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <hip/hip_runtime.h>
+
+#include "oeq.h"
+
+namespace oeq {
+namespace readout {
+
+struct DropoutArgs {
+    int64_t rows, cols;
+    const void *x, *residual;  // residual may be NULL
+    void *out;
+    int64_t ld_x, ld_residual, ld_out;
+    uint32_t threshold;
+    float scale;
+    const int64_t *rng;
+};
+hipError_t dropout(oeq_dtype dtype, const DropoutArgs &a, hipStream_t stream);
+
+struct GroupNormArgs {
+    int64_t rows;
+    int32_t n_struct, channels, groups, silu;
+    const int32_t *ptr;
+    const void *x;
+    int64_t ld_x;
+    const float *weight, *bias;  // either may be NULL (ones, zeros)
+    float eps;
+    float *mean, *rstd;  // written by the forward, read by the backward
+    void *out;           // forward
+    int64_t ld_out;
+    const void *grad_out;  // backward
+    int64_t ld_grad_out;
+    void *grad_x;
+    int64_t ld_grad_x;
+    float *grad_weight, *grad_bias;
+    void *workspace;
+};
+struct GroupNormBytes {
+    size_t fwd, bwd;
+};
+// Workspace bytes, and the workgroups of a launch.
+GroupNormBytes group_norm_workspace(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups);
+int64_t group_norm_blocks(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups);
+hipError_t group_norm_fwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream);
+hipError_t group_norm_bwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream);
+
+}  // namespace readout
+}  // namespace oeq

@@ -81,7 +81,9 @@ typedef enum {
     OEQ_ERR_JIT = 5          /* runtime compilation of the kernels failed    */
 } oeq_status;
 
-typedef enum { OEQ_F32 = 0, OEQ_F64 = 1 } oeq_dtype;
+/* Plans take OEQ_F32 and OEQ_F64; the readout operators (below) OEQ_F32, OEQ_F16 and
+ * OEQ_BF16. */
+typedef enum { OEQ_F32 = 0, OEQ_F64 = 1, OEQ_F16 = 2, OEQ_BF16 = 3 } oeq_dtype;
 
 /* How the x gradient is scattered to senders in the backward passes.
  * ATOMIC: hardware floating-point atomics (summation order varies run to run).
@@ -450,6 +452,81 @@ oeq_status oeq_tp_conv_bwd_radial(const oeq_plan *plan, int64_t n_nodes, int64_t
                                   void *grad_Y, void *grad_vec, void *grad_W1, void *grad_W2,
                                   oeq_bwd_mode mode, void *workspace, size_t workspace_bytes,
                                   void *stream);
+
+/* ---- Readout operators -------------------------------------------------------
+ * What a model does with node features after the convolutions: normalise them per
+ * structure, regularise them, and let query tokens of each structure attend to its
+ * atoms.  They take no plan.  Structures are stacked along the rows, and a row
+ * pointer ptr[n_struct + 1] (device, int32, ptr[0] = 0, non-decreasing,
+ * ptr[n_struct] = the number of rows) gives the rows of each; empty structures are
+ * fine.  As for the receiver CSR, the pointer's contents are the caller's
+ * responsibility (a pointer that leaves [0, rows] or decreases is cut to the range,
+ * so nothing outside the tensors is read or written, but the results mean nothing
+ * and rows that no structure holds are not written).
+ *
+ * dtype is OEQ_F32, OEQ_F16 or OEQ_BF16 (else OEQ_ERR_UNSUPPORTED); sums, statistics
+ * and products are accumulated in 32 bits or more and rounded once.  Strides count
+ * elements; the last dimension is contiguous.  Outputs must not overlap inputs,
+ * except that the dropout may run in place.  Otherwise the conventions of the other
+ * entry points hold: asynchronous on `stream`, host checks only, no allocation, no
+ * library state, workspaces 256-byte aligned.  Every result is bitwise repeatable:
+ * no floating-point atomics. */
+typedef enum { OEQ_ACT_NONE = 0, OEQ_ACT_SILU = 1 } oeq_act;
+
+/* Group norm, channels last, with an activation.  x [n_rows, C] (row stride
+ * x_stride >= C, so the scalar block of wider node rows is taken in place); groups of
+ * C / n_groups consecutive channels (n_groups divides C, C / n_groups <= 2048).  Over
+ * the n elements of a structure's rows in a group:
+ *   mean, var = mean and biased variance, rstd = 1 / sqrt(var + eps)
+ *   z = (x - mean) rstd weight[c] + bias[c],  out = z, or z / (1 + exp(-z)) for SILU
+ * weight and bias are fp32 [C], NULL for ones and zeros.  mean and rstd (fp32
+ * [n_struct, n_groups]) are written for the backward; an empty structure has mean 0
+ * and rstd 0.  eps > 0.  `workspace` must hold the bytes that
+ * oeq_group_norm_workspace_size gives for the direction (either pointer may be NULL;
+ * 0: no workspace is needed). */
+oeq_status oeq_group_norm_workspace_size(int64_t n_rows, int32_t n_struct, int32_t n_channels,
+                                         int32_t n_groups, size_t *fwd_bytes, size_t *bwd_bytes);
+oeq_status oeq_group_norm_fwd(oeq_dtype dtype, int64_t n_rows, int32_t n_struct, int32_t n_channels,
+                              int32_t n_groups, oeq_act act, double eps, const int32_t *ptr,
+                              const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, void *out, int64_t out_stride, float *mean,
+                              float *rstd, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of <grad_out, out>: with xhat = (x - mean) rstd, dz = grad_out * dout/dz,
+ * dh = dz weight and means over the n elements of the structure and group,
+ *   grad_x = rstd (dh - mean(dh) - xhat mean(dh xhat))   [n_rows, C]
+ *   grad_weight = sum over all rows of dz xhat, grad_bias = sum of dz   (fp32 [C])
+ * mean and rstd are the forward's.  Any gradient may be NULL (not computed).  With no
+ * rows the requested weight gradients are written as zeros. */
+oeq_status oeq_group_norm_bwd(oeq_dtype dtype, int64_t n_rows, int32_t n_struct, int32_t n_channels,
+                              int32_t n_groups, oeq_act act, const int32_t *ptr, const void *x,
+                              int64_t x_stride, const float *weight, const float *bias,
+                              const float *mean, const float *rstd, const void *grad_out,
+                              int64_t grad_out_stride, void *grad_x, int64_t grad_x_stride,
+                              float *grad_weight, float *grad_bias, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Dropout with a mask that is never stored: out = residual + x * keep / (1 - p'), a
+ * dropped element giving exactly residual (0 where residual is NULL), whatever x holds
+ * there.  x, residual and out are [n_rows, n_cols].  The mask is a function of the
+ * generator state and of (row, column) alone, not of strides or of dtype:
+ *   element (r, c) is dropped where u < t, with u the 16-bit part c % 8 (low half
+ *   first) of the Philox4x32-10 block of counter (c / 8, r, offset low, offset high)
+ *   and key (seed low, seed high), t = min(65535, floor(65536 p + 1/2)),
+ *   and 1 - p' = 1 - t / 65536, so that the expected value is x for the p' in use.
+ * rng is a device array {seed, offset}, read when the call runs: a captured graph draws
+ * other masks on each replay once the caller advances the offset on the device.
+ * 0 <= p < 1; n_rows < 2^32, n_cols < 2^31. */
+oeq_status oeq_dropout_fwd(oeq_dtype dtype, int64_t n_rows, int64_t n_cols, const void *x,
+                           int64_t x_stride, const void *residual, int64_t residual_stride,
+                           double p, const int64_t *rng, void *out, int64_t out_stride,
+                           void *stream);
+
+/* Gradient to x of <grad_out, out> for the same p and generator state:
+ * grad_x = grad_out * keep / (1 - p').  (The gradient to the residual is grad_out.) */
+oeq_status oeq_dropout_bwd(oeq_dtype dtype, int64_t n_rows, int64_t n_cols, const void *grad_out,
+                           int64_t grad_out_stride, double p, const int64_t *rng, void *grad_x,
+                           int64_t grad_x_stride, void *stream);
 
 /* Synchronously validates a receiver CSR on the device (rowptr monotone,
  * rowptr[0] = 0, rowptr[N] = E, 0 <= src < N).  Test helper: synchronises. */
