@@ -39,7 +39,7 @@ EXPORTED = ["oeq_plan_create", "oeq_plan_create_cached", "oeq_plan_destroy", "oe
             "oeq_radial_bwd", "oeq_tp_conv_fwd_radial", "oeq_workspace_size_radial", "oeq_tp_conv_bwd_radial",
             "oeq_tp_conv_fwd_pos", "oeq_workspace_size_pos", "oeq_tp_conv_bwd_pos",
             "oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
-            "oeq_dropout_bwd"]
+            "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd"]
 SCHEDULES = {0: "receiver", 1: "sender"}
 
 
@@ -63,6 +63,14 @@ class _Desc(ctypes.Structure):
                 ("y_lmax", ctypes.c_int32), ("out_irreps", ctypes.POINTER(_Irrep)),
                 ("n_out", ctypes.c_int32), ("paths", ctypes.POINTER(_Path)),
                 ("n_paths", ctypes.c_int32), ("lmax_out", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class _AttnDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_struct", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("q_rows", ctypes.c_int64),
+                ("k_rows", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("scale", ctypes.c_double), ("p_drop", ctypes.c_double)]
 
 
 _lib = None
@@ -160,6 +168,13 @@ def lib():
     L.oeq_dropout_fwd.restype = st
     L.oeq_dropout_bwd.argtypes = [I, I64, I64, P, I64, D, P, P, I64, P]
     L.oeq_dropout_bwd.restype = st
+    AD = ctypes.POINTER(_AttnDesc)
+    L.oeq_cross_attn_workspace_size.argtypes = [AD, SZP, SZP]
+    L.oeq_cross_attn_workspace_size.restype = st
+    L.oeq_cross_attn_fwd.argtypes = [AD] + [P] * 10 + [SZ, P]
+    L.oeq_cross_attn_fwd.restype = st
+    L.oeq_cross_attn_bwd.argtypes = [AD] + [P] * 14 + [SZ, P]
+    L.oeq_cross_attn_bwd.restype = st
     L.oeq_status_string.argtypes = [ctypes.c_int]
     L.oeq_status_string.restype = ctypes.c_char_p
     L.oeq_last_error.argtypes = []
@@ -851,3 +866,80 @@ def oeq_dropout_bwd(grad_out, p: float, rng, out=None):
     _check(lib().oeq_dropout_bwd(code, grad_out.shape[0], grad_out.shape[1], _ptr(grad_out), ld, float(p), _ptr(rng),
                                  _ptr(out), ld_o, _stream()))
     return out
+
+
+def _heads(t, shape, like, name):
+    """A [rows, heads, dim] operand with strided rows and heads: its two strides."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != like.device:
+        raise TypeError(f"{name} must be a tensor on {like.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    # the stride of a dimension of one is arbitrary: it is never stepped over
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
+    import torch
+    code = _elem(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, dim]")
+    Tq, H, D = q.shape
+    Tk, Hk = k.shape[0], k.shape[1]
+    qs, ks, vs = _heads(q, (Tq, H, D), q, "q"), _heads(k, (Tk, Hk, D), q, "k"), _heads(v, (Tk, Hk, D), q, "v")
+    B = q_ptr.shape[0] - 1
+    _want(q_ptr, (B + 1,), torch.int32, "q_ptr")
+    _want(k_ptr, (B + 1,), torch.int32, "k_ptr")
+    if key_mask is not None:
+        _want(key_mask, (Tk,), torch.bool if key_mask.dtype == torch.bool else torch.uint8, "key_mask")
+    _want(rng, (2,), torch.int64, "rng")
+    return _AttnDesc(code, B, H, Hk, D, Tq, Tk, *qs, *ks, *vs, D ** -0.5 if scale is None else float(scale),
+                     float(p_drop))
+
+
+def oeq_cross_attn_fwd(q, k, v, q_ptr, k_ptr, scale=None, key_mask=None, p_drop: float = 0.0, rng=None, out=None,
+                       lse=None, workspace=None):
+    """(out, lse): attention of q [Tq, H, D] to the states k, v [Tk, Hkv, D] of their structure
+    (q_ptr, k_ptr: row pointers over the same structures).  scale defaults to 1 / sqrt(D);
+    key_mask [Tk] (bool or uint8) is nonzero where a state is visible; rng (see
+    oeq_dropout_fwd) is needed for p_drop > 0.  lse is fp32 [Tq, H]."""
+    import torch
+    d = _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device)
+    if lse is None:
+        lse = _empty(q.shape[:2], torch.float32, q.device)
+    _want(out, q.shape, q.dtype, "out")
+    _want(lse, q.shape[:2], torch.float32, "lse")
+    need = ctypes.c_size_t()
+    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), ctypes.byref(need), None))
+    ws, nbytes = _scratch(need.value, workspace, q.device)
+    _check(lib().oeq_cross_attn_fwd(ctypes.byref(d), _ptr(q_ptr), _ptr(k_ptr), _ptr(q), _ptr(k), _ptr(v),
+                                    _ptr(key_mask), _ptr(rng), _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream()))
+    return out, lse
+
+
+def oeq_cross_attn_bwd(q, k, v, q_ptr, k_ptr, out, lse, grad_out, scale=None, key_mask=None, p_drop: float = 0.0,
+                       rng=None, need=("q", "k", "v"), grads=None, workspace=None):
+    """(grad_q, grad_k, grad_v) of <grad_out, out> from the forward's operands, out and lse;
+    entries not in `need` are None.  `grads` may supply preallocated gradients."""
+    import torch
+    d = _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
+    _want(out, q.shape, q.dtype, "out")
+    _want(lse, q.shape[:2], torch.float32, "lse")
+    _want(grad_out, q.shape, q.dtype, "grad_out")
+    shapes = (q.shape, k.shape, k.shape)
+    if grads is None:
+        grads = tuple(_empty(s, q.dtype, q.device) if n in need else None for n, s in zip(("q", "k", "v"), shapes))
+    gq, gk, gv = (_want(t, s, q.dtype, "grad_" + n) for t, s, n in zip(grads, shapes, ("q", "k", "v")))
+    nb = ctypes.c_size_t()
+    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), None, ctypes.byref(nb)))
+    ws, nbytes = _scratch(nb.value, workspace, q.device)
+    _check(lib().oeq_cross_attn_bwd(ctypes.byref(d), _ptr(q_ptr), _ptr(k_ptr), _ptr(q), _ptr(k), _ptr(v),
+                                    _ptr(key_mask), _ptr(rng), _ptr(out), _ptr(lse), _ptr(grad_out), _ptr(gq),
+                                    _ptr(gk), _ptr(gv), _ptr(ws), nbytes, _stream()))
+    return gq, gk, gv

@@ -22,7 +22,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["capi.cpp", "capi_graph.cpp", "capi_edge.cpp", "capi_readout.cpp", "planner.cpp", "cg_tables.cpp", "codegen.cpp",
                 "jit.cpp"]
-HIP_SOURCES = ["csr.hip", "noalloc.hip", "group_norm.hip", "dropout.hip"]
+HIP_SOURCES = ["csr.hip", "noalloc.hip", "group_norm.hip", "dropout.hip", "cross_attn_fwd.hip", "cross_attn_bwd.hip"]
 ARCH = "gfx950"
 NO_PACKED_FP32 = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

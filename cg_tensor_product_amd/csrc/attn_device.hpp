@@ -1,0 +1,165 @@
+// Device pieces shared by the cross-attention kernels: matrix products of 32 x 32 tiles,
+// tiles of rows in LDS and how a wave takes operands from them.
+//
+// One 32 x 32 x 16 step multiplies A [32, 16] by B [16, 32].  Lane l holds, with
+// half = l / 32, the elements k = 8 half .. 8 half + 7 of row l % 32 of A, and the same of
+// column l % 32 of B.  fp16 and bf16 have it as one instruction; fp32 takes eight
+// 32 x 32 x 2 instructions, the j-th over the j-th elements of both halves, so that all
+// types share one layout.  Of the result the lane holds column l % 32 and the rows
+// 8 (i / 4) + 4 half + i % 4 (i = 0..15).
+//
+// Score tiles are computed with the rows of A permuted, row m holding key (or query)
+// 16 (m / 16) + 8 (m / 4 % 2) + 4 (m / 8 % 2) + m % 4 of the tile.  Then lane l's sixteen
+// results are the keys 16 s + 8 half + j (i = 8 s + j): exactly its operand of the next
+// product's steps s = 0, 1, so probabilities go from one product into the next in
+// registers, and eight consecutive keys share one block of the dropout generator.
+#pragma once
+
+#include <type_traits>
+
+#include "readout.hpp"
+#include "readout_device.hpp"
+
+namespace oeq {
+namespace readout {
+
+using f32x16 = float __attribute__((ext_vector_type(16)));
+using i16x4 = short __attribute__((ext_vector_type(4)));
+using i16x8 = vec8<short>;
+
+constexpr float kLog2E = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ f32x16 mma(f32x16 acc, vec8<bf16> a, vec8<bf16> b) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(f32x16 acc, vec8<f16> a, vec8<f16> b) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(f32x16 acc, f32x8 a, f32x8 b) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], acc, 0, 0, 0);
+    return acc;
+}
+
+// Elements from one tile row to the next: 16 bytes past the row, an odd number of 16-byte
+// pieces, so that 16 consecutive rows start in different banks.
+template <class T, int kDim>
+constexpr int kTileRow = kDim + 16 / int(sizeof(T));
+
+__device__ __forceinline__ int permuted_row(int m) { return (m & 16) | (m & 4) << 1 | (m & 8) >> 1 | (m & 3); }
+
+// A operand: row `row` of the tile, step d0 / 16.
+template <class T>
+__device__ __forceinline__ vec8<T> row_operand(const T *tile, int tile_row, int row, int d0, int half) {
+    return *reinterpret_cast<const vec8<T> *>(tile + row * tile_row + d0 + 8 * half);
+}
+template <>
+__device__ __forceinline__ f32x8 row_operand<float>(const float *tile, int tile_row, int row, int d0, int half) {
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(tile + row * tile_row + d0 + 8 * half);
+    const f32x4 a = p[0], b = p[1];
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A operand from the transposed tile: column d0 + lane % 32, rows row0 + 8 half + j.  The
+// 16-bit form is two transposing LDS reads: of each 16 lanes the address of lane i is that of
+// four elements, row i / 4, and the lane receives column i of the four rows.
+template <class T>
+__device__ __forceinline__ vec8<T> column_operand(const T *tile, int tile_row, int row0, int d0, int lane) {
+    const int half = lane >> 5, group = lane >> 4 & 1, i = lane & 15;
+    const T *p = tile + (row0 + 8 * half + (i >> 2)) * tile_row + d0 + 16 * group + (i & 3) * 4;
+    using Lds = __attribute__((address_space(3))) i16x4 *;
+    const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p));
+    const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * tile_row));
+    const i16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(vec8<T>, v);
+}
+template <>
+__device__ __forceinline__ f32x8 column_operand<float>(const float *tile, int tile_row, int row0, int d0, int lane) {
+    const float *p = tile + (row0 + 8 * (lane >> 5)) * tile_row + d0 + (lane & 31);
+    f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[j * tile_row];
+    return v;
+}
+
+// Rows of a strided operand on their way to LDS: kRows x kDim elements by kThreads threads,
+// in pieces of eight.  `fetch` reads rows first .. first + kRows - 1, rows past `last` in place
+// of which row `last` is read (its values are not used); `store` writes them, with zeros for
+// rows whose bit is not set and for columns past the head's dimension.
+template <class T, int kRows, int kDim, int kThreads>
+struct RowStage {
+    static constexpr int kPerRow = kDim / 8, kTotal = kRows * kPerRow, kPieces = (kTotal + kThreads - 1) / kThreads;
+    vec8<T> v[kPieces];
+
+    template <class RowAddress>
+    __device__ __forceinline__ void fetch(int thread, int dim, RowAddress &&address) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int piece = thread + i * kThreads, row = piece / kPerRow, d = piece % kPerRow * 8;
+            if (piece < kTotal && d < dim) v[i] = *reinterpret_cast<const vec8<T> *>(address(row) + d);
+        }
+    }
+    __device__ __forceinline__ void store(T *tile, int thread, int dim, uint64_t valid) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int piece = thread + i * kThreads, row = piece / kPerRow, d = piece % kPerRow * 8;
+            if (piece >= kTotal) continue;  // decided at compile time where the pieces divide evenly
+            vec8<T> o = v[i];
+            if (d >= dim || !(valid >> row & 1)) o = vec8<T>(T(0.f));
+            T *at = tile + row * kTileRow<T, kDim> + d;
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<f32x4 *>(at)[0] = __builtin_shufflevector(o, o, 0, 1, 2, 3);
+                reinterpret_cast<f32x4 *>(at)[1] = __builtin_shufflevector(o, o, 4, 5, 6, 7);
+            } else {
+                *reinterpret_cast<vec8<T> *>(at) = o;
+            }
+        }
+    }
+};
+
+// Orders a wave's own LDS writes before its reads (LDS serves a wave in order; this keeps the
+// compiler from moving them).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Value of the lane 32 away.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// Which structure, key head and rows a workgroup has.  Query rows of one key head are
+// numbered r = query * share + head within the share, so heads that share keys share the tile.
+struct Place {
+    int kv_head, split;
+    int64_t q_begin, k_begin;  // first rows of the structure
+    int rows, keys;            // query rows times share; keys
+    int first;                 // first row (or key) of the tile
+    bool any;
+};
+
+template <int kTile>
+__device__ __forceinline__ Place place_of(const AttnArgs &a, bool by_query, int splits, int64_t slots) {
+    Place p;
+    int64_t item = blockIdx.x;
+    p.split = static_cast<int>(item % splits);
+    item /= splits;
+    const int64_t slot = item % slots;
+    p.kv_head = static_cast<int>(item / slots);
+    int64_t first;
+    const int32_t *ptr = by_query ? a.q_ptr : a.k_ptr;
+    const int per = by_query ? a.share : 1;
+    const int b = find_structure(ptr, a.n_struct, per, kTile, slot, &first);
+    const Span q = span_of(a.q_ptr, b, a.q_rows), k = span_of(a.k_ptr, b, a.k_rows);
+    p.q_begin = q.begin;
+    p.k_begin = k.begin;
+    p.rows = static_cast<int>((q.end - q.begin) * a.share);
+    p.keys = static_cast<int>(k.end - k.begin);
+    const int64_t at = (slot - first) * kTile;
+    p.first = static_cast<int>(at);
+    p.any = at >= 0 && at < (by_query ? p.rows : p.keys);
+    return p;
+}
+
+}  // namespace readout
+}  // namespace oeq

@@ -99,6 +99,15 @@ oeq_status check_group_norm(oeq_dtype dtype, oeq_act act, const ro::GroupNormArg
     return OEQ_OK;
 }
 
+// The drop threshold and the factor of what is kept.
+oeq_status drop_of(double p, uint32_t *threshold, float *scale) {
+    if (!(p >= 0.0 && p < 1.0)) return fail(OEQ_ERR_INVALID_ARG, "the drop probability must be in [0, 1)");
+    const double t = std::floor(65536.0 * p + 0.5);
+    *threshold = static_cast<uint32_t>(t > 65535.0 ? 65535.0 : t);
+    *scale = static_cast<float>(65536.0 / (65536.0 - *threshold));
+    return OEQ_OK;
+}
+
 // ---- dropout ------------------------------------------------------------------------------
 
 oeq_status run_dropout(oeq_dtype dtype, ro::DropoutArgs a, double p, hipStream_t stream) {
@@ -106,7 +115,7 @@ oeq_status run_dropout(oeq_dtype dtype, ro::DropoutArgs a, double p, hipStream_t
     if (a.rows < 0 || a.cols < 0) return fail(OEQ_ERR_INVALID_ARG, "negative size");
     if (a.rows >> 32 || a.cols >= kMaxRows)
         return fail(OEQ_ERR_UNSUPPORTED, "rows must be below 2^32 and columns below 2^31");
-    if (!(p >= 0.0 && p < 1.0)) return fail(OEQ_ERR_INVALID_ARG, "p must be in [0, 1)");
+    OEQ_TRY(drop_of(p, &a.threshold, &a.scale));
     if (!a.rng) return fail(OEQ_ERR_INVALID_ARG, "rng is NULL");
     OEQ_TRY(check_aligned(a.rng, 8, "rng"));
     if (a.rows == 0 || a.cols == 0) return OEQ_OK;
@@ -117,10 +126,58 @@ oeq_status run_dropout(oeq_dtype dtype, ro::DropoutArgs a, double p, hipStream_t
     OEQ_TRY(check_aligned(a.x, es, "the input"));
     OEQ_TRY(check_aligned(a.out, es, "the output"));
     OEQ_TRY(check_aligned(a.residual, es, "residual"));
-    const double t = std::floor(65536.0 * p + 0.5);
-    a.threshold = static_cast<uint32_t>(t > 65535.0 ? 65535.0 : t);
-    a.scale = static_cast<float>(65536.0 / (65536.0 - a.threshold));
     return from_hip(ro::dropout(dtype, a, stream), "dropout");
+}
+
+// ---- cross attention ---------------------------------------------------------------------------
+
+// Sizes and types of a descriptor; fills what the launchers take from it.
+oeq_status attn_args(const oeq_attn_desc *d, ro::AttnArgs *a) {
+    if (!d) return fail(OEQ_ERR_INVALID_ARG, "the descriptor is NULL");
+    OEQ_TRY(check_dtype(d->dtype));
+    if (d->n_struct < 0 || d->q_rows < 0 || d->k_rows < 0) return fail(OEQ_ERR_INVALID_ARG, "negative size");
+    if (d->n_heads < 1 || d->n_kv_heads < 1 || d->n_heads % d->n_kv_heads)
+        return fail(OEQ_ERR_INVALID_ARG, "n_kv_heads must divide n_heads");
+    if (d->head_dim < 1) return fail(OEQ_ERR_INVALID_ARG, "head_dim must be positive");
+    if (d->head_dim % 8 || d->head_dim > 128)
+        return fail(OEQ_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 and at most 128");
+    if (d->n_struct == 0 && (d->q_rows || d->k_rows)) return fail(OEQ_ERR_INVALID_ARG, "rows without structures");
+    constexpr int64_t most = int64_t(1) << 31;
+    if (d->q_rows >= most / d->n_heads || d->k_rows >= most - 1024)
+        return fail(OEQ_ERR_UNSUPPORTED, "query rows times heads, and states, must be below 2^31");
+    if (!(d->scale > 0.0) || !std::isfinite(static_cast<float>(d->scale)) || !(static_cast<float>(d->scale) > 0.f))
+        return fail(OEQ_ERR_INVALID_ARG, "scale must be positive and finite");
+    *a = ro::AttnArgs{};
+    a->n_struct = d->n_struct, a->heads = d->n_heads, a->kv_heads = d->n_kv_heads;
+    a->share = d->n_heads / d->n_kv_heads, a->dim = d->head_dim, a->q_rows = d->q_rows, a->k_rows = d->k_rows;
+    a->q_row = d->q_stride, a->q_head = d->q_head_stride, a->k_row = d->k_stride, a->k_head = d->k_head_stride;
+    a->v_row = d->v_stride, a->v_head = d->v_head_stride, a->scale = static_cast<float>(d->scale);
+    OEQ_TRY(drop_of(d->p_drop, &a->threshold, &a->keep_scale));
+    const int64_t es = static_cast<int64_t>(element_size(d->dtype));
+    for (int64_t stride : {a->q_row, a->q_head, a->k_row, a->k_head, a->v_row, a->v_head})
+        if (stride < 0 || stride * es % 16)
+            return fail(OEQ_ERR_INVALID_ARG, "strides must be non-negative multiples of 16 bytes");
+    constexpr int64_t grid = int64_t(1) << 24;  // a launch holds fewer than 2^32 threads
+    if (d->n_struct && (ro::cross_attn_fwd_blocks(*a) >= grid || ro::cross_attn_bwd_blocks(*a) >= grid))
+        return fail(OEQ_ERR_UNSUPPORTED, "too many rows and heads for one launch");
+    return OEQ_OK;
+}
+
+// The operands both directions read.
+oeq_status attn_operands(ro::AttnArgs *a, const int32_t *q_ptr, const int32_t *k_ptr, const void *q, const void *k,
+                         const void *v, const uint8_t *key_mask, const int64_t *rng) {
+    if (a->n_struct && (!q_ptr || !k_ptr)) return fail(OEQ_ERR_INVALID_ARG, "a row pointer is NULL");
+    if (a->q_rows && !q) return fail(OEQ_ERR_INVALID_ARG, "q is NULL");
+    if (a->k_rows && (!k || !v)) return fail(OEQ_ERR_INVALID_ARG, "k or v is NULL");
+    if (a->threshold && !rng) return fail(OEQ_ERR_INVALID_ARG, "dropout needs rng");
+    OEQ_TRY(check_aligned(q_ptr, 4, "q_ptr"));
+    OEQ_TRY(check_aligned(k_ptr, 4, "k_ptr"));
+    OEQ_TRY(check_aligned(q, 16, "q"));
+    OEQ_TRY(check_aligned(k, 16, "k"));
+    OEQ_TRY(check_aligned(v, 16, "v"));
+    OEQ_TRY(check_aligned(rng, 8, "rng"));
+    a->q_ptr = q_ptr, a->k_ptr = k_ptr, a->q = q, a->k = k, a->v = v, a->key_mask = key_mask, a->rng = rng;
+    return OEQ_OK;
 }
 
 }  // namespace
@@ -204,6 +261,55 @@ oeq_status oeq_dropout_bwd(oeq_dtype dtype, int64_t n_rows, int64_t n_cols, cons
         a.rows = n_rows, a.cols = n_cols, a.x = grad_out, a.ld_x = grad_out_stride;
         a.rng = rng, a.out = grad_x, a.ld_out = grad_x_stride;
         return run_dropout(dtype, a, p, static_cast<hipStream_t>(stream));
+    });
+}
+
+oeq_status oeq_cross_attn_workspace_size(const oeq_attn_desc *desc, size_t *fwd_bytes, size_t *bwd_bytes) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(attn_args(desc, &a));
+        if (fwd_bytes) *fwd_bytes = a.n_struct && a.q_rows ? ro::cross_attn_fwd_workspace(a) : 0;
+        if (bwd_bytes) *bwd_bytes = a.n_struct ? ro::cross_attn_bwd_workspace(a) : 0;
+        return OEQ_OK;
+    });
+}
+
+oeq_status oeq_cross_attn_fwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr, const void *q,
+                              const void *k, const void *v, const uint8_t *key_mask, const int64_t *rng, void *out,
+                              float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(attn_args(desc, &a));
+        OEQ_TRY(attn_operands(&a, q_ptr, k_ptr, q, k, v, key_mask, rng));
+        if (a.q_rows == 0) return OEQ_OK;
+        if (!out || !lse) return fail(OEQ_ERR_INVALID_ARG, "out or lse is NULL");
+        OEQ_TRY(check_aligned(out, 16, "out"));
+        OEQ_TRY(check_aligned(lse, 4, "lse"));
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_fwd_workspace(a)));
+        a.out = out, a.lse = lse, a.workspace = workspace;
+        return from_hip(ro::cross_attn_fwd(desc->dtype, a, static_cast<hipStream_t>(stream)), "cross attention");
+    });
+}
+
+oeq_status oeq_cross_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr, const void *q,
+                              const void *k, const void *v, const uint8_t *key_mask, const int64_t *rng,
+                              const void *out, const float *lse, const void *grad_out, void *grad_q, void *grad_k,
+                              void *grad_v, void *workspace, size_t workspace_bytes, void *stream) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(attn_args(desc, &a));
+        OEQ_TRY(attn_operands(&a, q_ptr, k_ptr, q, k, v, key_mask, rng));
+        if (a.q_rows && (!out || !lse || !grad_out)) return fail(OEQ_ERR_INVALID_ARG, "out, lse or grad_out is NULL");
+        for (const void *p : {out, grad_out, static_cast<const void *>(grad_q), static_cast<const void *>(grad_k),
+                              static_cast<const void *>(grad_v)})
+            OEQ_TRY(check_aligned(p, 16, "out, grad_out and the gradients"));
+        OEQ_TRY(check_aligned(lse, 4, "lse"));
+        if (a.n_struct == 0 || (!grad_q && !grad_k && !grad_v)) return OEQ_OK;
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_bwd_workspace(a)));
+        a.out = const_cast<void *>(out), a.lse = const_cast<float *>(lse), a.grad_out = grad_out;
+        a.grad_q = grad_q, a.grad_k = grad_k, a.grad_v = grad_v, a.workspace = workspace;
+        return from_hip(ro::cross_attn_bwd(desc->dtype, a, static_cast<hipStream_t>(stream)),
+                        "cross attention backward");
     });
 }
 

@@ -1,0 +1,383 @@
+// Cross attention forward.  For the visible keys of a query row's structure
+//   s = scale q k^T,  lse = log sum exp s,  p = exp(s - lse),  out = (p * keep) v
+// in one pass over the keys with a running maximum and sum.
+//
+// A wave computes S^T = K Q^T tile by tile with its 32 query rows along the lanes, so the
+// softmax statistics are one number a lane, and O^T = V^T P^T takes the probabilities
+// straight from the score registers (attn_device.hpp).  K and V pass through LDS; V's
+// operand is read transposed from it.
+//
+// Two ways to split the work (kSplitKeys):
+//   false: the four waves own 32 query rows each and share tiles of 64 keys;
+//   true:  for few query rows (single tokens, small structures) the four waves share 32 rows
+//          and take tiles of 32 keys in turn, each through LDS of its own and without
+//          barriers; their results are joined in LDS at the end.
+// With few workgroups the keys are also split over workgroups; a second kernel joins them.
+#include "attn_device.hpp"
+
+namespace oeq {
+namespace readout {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+// The running maximum may lag behind by this many powers of two before the sums are scaled.
+constexpr float kLag = 8.f;
+
+template <class T, int kDim, bool kSplitKeys>
+struct Tiles {
+    static constexpr int kKeys = kSplitKeys ? 32 : 64;
+    static constexpr int kRow = kTileRow<T, kDim>;
+    static constexpr int kRows = kSplitKeys ? 32 : 128;  // query rows of a workgroup
+    static constexpr int kStage = kSplitKeys ? 64 : kThreads;
+    static constexpr int kTile = kKeys * kRow;  // elements of one K or V tile
+    static constexpr int kLds = (kSplitKeys ? kWaves : 1) * 2 * kTile * int(sizeof(T));
+    static constexpr int kJoinRow = kDim + 4;
+    static constexpr int kJoin = kSplitKeys ? kWaves * 32 * (kJoinRow + 2) * 4 : 0;
+    static constexpr int kBytes = kLds > kJoin ? kLds : kJoin;
+};
+
+struct Partial {
+    float *out;  // [split][query row, head][dim], normalised
+    float *lse;  // [split][query row, head], in powers of two
+};
+
+template <class T, int kDim, bool kDrop, bool kSplitKeys>
+__global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, int64_t slots, Partial partial) {
+    using C = Tiles<T, kDim, kSplitKeys>;
+    constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32, kSub = kKeys / 32;
+    __shared__ __attribute__((aligned(16))) char lds[C::kBytes];
+    const Place w = place_of<C::kRows>(a, true, splits, slots);
+    if (!w.any) return;
+    const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+    const int thread = kSplitKeys ? lane : threadIdx.x;
+    T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
+
+    // this lane's query row
+    const int r = w.first + (kSplitKeys ? 0 : wave * 32) + (lane & 31);
+    const bool row_ok = r < w.rows;
+    const int64_t q_row = w.q_begin + (row_ok ? r / a.share : 0);
+    const int head = w.kv_head * a.share + (row_ok ? r % a.share : 0);
+    vec8<T> qf[kSteps];
+    {
+        const T *q = static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            qf[s] = row_ok && d < a.dim ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
+        }
+    }
+    Rng g{};
+    if (kDrop) g = load_rng(a.rng);
+    const uint32_t drop_row = static_cast<uint32_t>(q_row * a.heads + head);
+
+    const float c = a.scale * kLog2E;
+    f32x16 o[kOut] = {};
+    float top = -INFINITY, sum = 0.f;  // the running maximum (unscaled) and this half's sum
+
+    // this workgroup's keys, in whole tiles
+    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
+    const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
+    const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
+    const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
+    const uint8_t *mask = a.key_mask ? a.key_mask + w.k_begin : nullptr;
+
+    RowStage<T, kKeys, kDim, C::kStage> k_in, v_in;
+    uint32_t visible = 0;
+    auto fetch = [&](int t) {
+        const int k0 = t * kKeys, last = w.keys - 1;
+        const int key = k0 + (lane & (kKeys - 1));
+        visible = key <= last && (!mask || mask[key]);
+        k_in.fetch(thread, a.dim, [&](int row) { return k_base + int64_t(min(k0 + row, last)) * a.k_row; });
+        v_in.fetch(thread, a.dim, [&](int row) { return v_base + int64_t(min(k0 + row, last)) * a.v_row; });
+    };
+
+    int t = w.split * per + (kSplitKeys ? wave : 0);
+    if (t < t_end) fetch(t);
+    for (; t < t_end; t += t_step) {
+        const uint64_t valid = __ballot(visible);
+        if (kSplitKeys) wave_sync(); else __syncthreads();  // the last tile has been read
+        k_in.store(k_tile, thread, a.dim, valid);
+        v_in.store(v_tile, thread, a.dim, valid);
+        if (kSplitKeys) wave_sync(); else __syncthreads();
+        const int k0 = t * kKeys;
+        if (t + t_step < t_end) fetch(t + t_step);
+
+        f32x16 s[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            s[u] = f32x16{};
+            const int row = 32 * u + permuted_row(lane & 31);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) s[u] = mma(s[u], row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
+        }
+        const uint64_t all = kKeys == 64 ? ~0ull : 0xffffffffull;
+        if ((valid & all) != all) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = 32 * u + 16 * (i >> 3) + 8 * half + (i & 7);
+                    if (!(valid >> key & 1)) s[u][i] = -INFINITY;
+                }
+            }
+        }
+        float high = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) high = fmaxf(high, s[u][i]);
+        }
+        high = fmaxf(high, other_half(high));
+        // top = -inf (nothing seen yet) always moves on; a row that has seen nothing stays there
+        if (__any((high - top) * c > kLag || (top == -INFINITY && high > -INFINITY))) {
+            const float now = fmaxf(top, high);
+            const float scale = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((top - now) * c);
+            sum *= scale;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) o[d] *= scale;
+            top = now;
+        }
+        const float shift = top == -INFINITY ? 0.f : top * c;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            vec8<T> p[2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -shift));
+                sum += e;
+                s[u][i] = e;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x8 e;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = s[u][8 * h + j];
+                if (kDrop) {
+                    const uint32_t keep = keep_bits(g, (k0 + 32 * u + 16 * h) / 8 + half, drop_row, a.threshold);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = (keep >> j & 1) ? e[j] : 0.f;
+                }
+                p[h] = from_f32<T>(e);
+            }
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+                o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u, 32 * d, lane), p[0]);
+                o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u + 16, 32 * d, lane), p[1]);
+            }
+        }
+    }
+    sum += other_half(sum);
+
+    const int64_t at = q_row * a.heads + head;
+    if (!kSplitKeys) {
+        if (!row_ok) return;
+        const float lse2 = sum > 0.f || sum != sum ? top * c + __builtin_amdgcn_logf(sum) : -INFINITY;
+        const float norm = sum > 0.f || sum != sum ? a.keep_scale / sum : 0.f;
+        if (splits > 1) {
+            const int64_t to = int64_t(w.split) * a.q_rows * a.heads + at;
+            if (half == 0) partial.lse[to] = lse2;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = 32 * d + 8 * i + 4 * half;
+                    if (col < a.dim) {
+                        const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+                        *reinterpret_cast<f32x4 *>(partial.out + to * a.dim + col) = v * norm;
+                    }
+                }
+            }
+            return;
+        }
+        if (half == 0) a.lse[at] = lse2 * kLn2;
+        T *out = static_cast<T *>(a.out) + at * a.dim;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = 32 * d + 8 * i + 4 * half;
+                if (col < a.dim) {
+                    using V4 = T __attribute__((ext_vector_type(4)));
+                    const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+                    *reinterpret_cast<V4 *>(out + col) = __builtin_convertvector(v * norm, V4);
+                }
+            }
+        }
+        return;
+    }
+
+    // join the four waves: every one has its own maximum, sum and output for the same 32 rows
+    __syncthreads();
+    float *join = reinterpret_cast<float *>(lds), *join_top = join + kWaves * 32 * C::kJoinRow,
+          *join_sum = join_top + kWaves * 32;
+    float *mine = join + (wave * 32 + (lane & 31)) * C::kJoinRow;
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            *reinterpret_cast<f32x4 *>(mine + 32 * d + 8 * i + 4 * half) = v;
+        }
+    }
+    if (half == 0) {
+        join_top[wave * 32 + lane] = top;
+        join_sum[wave * 32 + lane] = sum;
+    }
+    __syncthreads();
+    const int jr = threadIdx.x >> 3, jc = threadIdx.x & 7, row = w.first + jr;  // eight threads a row
+    if (row >= w.rows) return;
+    float most = -INFINITY, total = 0.f, weight[kWaves];
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) most = fmaxf(most, join_top[i * 32 + jr]);
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        const float m = join_top[i * 32 + jr];
+        weight[i] = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - most) * c);
+        // a wave that saw nothing has a zero sum; one that saw a NaN has a NaN
+        total += join_sum[i * 32 + jr] * (m == -INFINITY ? 1.f : weight[i]);
+    }
+    const bool seen = total > 0.f || total != total;
+    const float lse2 = seen ? most * c + __builtin_amdgcn_logf(total) : -INFINITY;
+    const float norm = seen ? a.keep_scale / total : 0.f;
+    const int64_t q_out = (w.q_begin + row / a.share) * a.heads + w.kv_head * a.share + row % a.share;
+    const int64_t to = int64_t(w.split) * a.q_rows * a.heads + q_out;
+    if (jc == 0) {
+        if (splits > 1)
+            partial.lse[to] = lse2;
+        else
+            a.lse[q_out] = lse2 * kLn2;
+    }
+    for (int col = jc * 8; col < a.dim; col += 64) {
+        f32x8 v = {};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const float *from = join + (i * 32 + jr) * C::kJoinRow + col;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += from[j] * weight[i];
+        }
+        v *= norm;
+        if (splits > 1)
+            store8(partial.out + to * a.dim + col, v);
+        else
+            store8(static_cast<T *>(a.out) + q_out * a.dim + col, from_f32<T>(v));
+    }
+}
+
+// Joins the splits of one (query row, head) a wave.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Partial partial) {
+    const int64_t n = a.q_rows * a.heads, at = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+    if (at >= n) return;
+    const int lane = threadIdx.x & 63;
+    const float mine = lane < splits ? partial.lse[lane * n + at] : -INFINITY;  // at most 64 splits
+    float most = mine;
+    for (int off = 32; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
+    const float weight = mine == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - most);
+    float total = weight;
+    for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off);
+    const bool seen = total > 0.f || total != total;
+    if (lane == 0) a.lse[at] = seen ? (most + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+    const float norm = seen ? 1.f / total : 0.f;
+    T *out = static_cast<T *>(a.out) + at * a.dim;
+    for (int d = lane * 2; d < a.dim; d += 128) {
+        float u = 0.f, v = 0.f;
+        for (int i = 0; i < splits; ++i) {
+            const float *p = partial.out + (i * n + at) * a.dim + d;
+            const float w = __shfl(weight, i);
+            u += p[0] * w;
+            v += p[1] * w;
+        }
+        out[d] = T(u * norm);
+        out[d + 1] = T(v * norm);
+    }
+}
+
+constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
+
+struct Choice {
+    bool split_keys;
+    int splits;
+    int64_t slots, blocks;
+};
+
+Choice choose(const AttnArgs &a) {
+    Choice c;
+    const int64_t rows = a.q_rows * a.share;
+    c.split_keys = rows <= 32 * int64_t(a.n_struct);
+    c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
+    const int64_t base = c.slots * a.kv_heads, most = a.k_rows / a.n_struct / 256;  // 256 keys a split at least
+    int64_t splits = (512 + base - 1) / base;  // two workgroups a compute unit
+    splits = splits > most ? most : splits;
+    c.splits = static_cast<int>(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    c.blocks = base * c.splits;
+    return c;
+}
+
+template <class T, int kDim, bool kDrop>
+void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(c.blocks)), threads(kThreads);
+    if (c.split_keys)
+        k_forward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
+    else
+        k_forward<T, kDim, kDrop, false><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
+}
+
+template <class T, int kDim>
+void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStream_t stream) {
+    if (a.threshold)
+        launch<T, kDim, true>(a, c, partial, stream);
+    else
+        launch<T, kDim, false>(a, c, partial, stream);
+}
+
+size_t partial_out(const AttnArgs &a, const Choice &c) {
+    return up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * a.dim * sizeof(float));
+}
+
+template <class T>
+hipError_t forward(const AttnArgs &a, hipStream_t stream) {
+    const Choice c = choose(a);
+    Partial partial{};
+    if (c.splits > 1) {
+        partial.out = static_cast<float *>(a.workspace);
+        partial.lse = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + partial_out(a, c));
+    }
+    if (a.dim <= 32)
+        launch<T, 32>(a, c, partial, stream);
+    else if (a.dim <= 64)
+        launch<T, 64>(a, c, partial, stream);
+    else if (a.dim <= 96)
+        launch<T, 96>(a, c, partial, stream);
+    else
+        launch<T, 128>(a, c, partial, stream);
+    if (c.splits > 1) {
+        const int64_t n = a.q_rows * a.heads;
+        k_join<T><<<dim3(static_cast<unsigned>((n + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a, c.splits,
+                                                                                                       partial);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t cross_attn_fwd_workspace(const AttnArgs &a) {
+    const Choice c = choose(a);
+    if (c.splits == 1) return 0;
+    return partial_out(a, c) + up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * sizeof(float));
+}
+
+int64_t cross_attn_fwd_blocks(const AttnArgs &a) { return choose(a).blocks; }
+
+hipError_t cross_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
+    switch (dtype) {
+        case OEQ_F32: return forward<float>(a, stream);
+        case OEQ_F16: return forward<f16>(a, stream);
+        case OEQ_BF16: return forward<bf16>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace readout
+}  // namespace oeq

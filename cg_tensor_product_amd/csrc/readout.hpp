@@ -50,5 +50,31 @@ int64_t group_norm_blocks(int64_t rows, int32_t n_struct, int32_t channels, int3
 hipError_t group_norm_fwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream);
 hipError_t group_norm_bwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream);
 
+struct AttnArgs {
+    int32_t n_struct, heads, kv_heads, share;  // share = heads / kv_heads
+    int32_t dim;
+    int64_t q_rows, k_rows;
+    const int32_t *q_ptr, *k_ptr;
+    const uint8_t *key_mask;  // may be NULL
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;  // strides
+    float scale;
+    uint32_t threshold;  // of the dropout; 0: none
+    float keep_scale;
+    const int64_t *rng;
+    void *out;  // written by the forward, read by the backward
+    float *lse;
+    const void *grad_out;  // backward
+    void *grad_q, *grad_k, *grad_v;
+    void *workspace;
+};
+// Workspace bytes and the workgroups of the largest launch of each direction.
+size_t cross_attn_fwd_workspace(const AttnArgs &a);
+size_t cross_attn_bwd_workspace(const AttnArgs &a);
+int64_t cross_attn_fwd_blocks(const AttnArgs &a);
+int64_t cross_attn_bwd_blocks(const AttnArgs &a);
+hipError_t cross_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
+hipError_t cross_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
+
 }  // namespace readout
 }  // namespace oeq

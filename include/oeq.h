@@ -528,6 +528,56 @@ oeq_status oeq_dropout_bwd(oeq_dtype dtype, int64_t n_rows, int64_t n_cols, cons
                            int64_t grad_out_stride, double p, const int64_t *rng, void *grad_x,
                            int64_t grad_x_stride, void *stream);
 
+/* Cross attention from query rows to the states (keys and values) of their own structure,
+ * of another length: structure b has the query rows q_ptr[b]..q_ptr[b+1] and the states
+ * k_ptr[b]..k_ptr[b+1] (two row pointers over the same n_struct structures).
+ * q [q_rows, H, D], k and v [k_rows, Hkv, D]; Hkv divides H and head h reads key head
+ * h / (H / Hkv); D a multiple of 8, at most 128.  For a query row over the states its
+ * structure holds and key_mask (uint8 [k_rows], nonzero = visible; NULL: all) leaves:
+ *   s = scale q k^T,  lse = log sum exp s,  p = exp(s - lse),  out = (p keep / (1 - p')) v
+ * with the dropout of oeq_dropout_fwd applied to p: its row is (query row) H + h, its
+ * column the state's number within the structure (p_drop 0: none, rng may be NULL).
+ * A row that sees nothing gives out = 0 and lse = -infinity; states that are not visible
+ * are never used, whatever they hold.
+ *
+ * One query row per structure (a serving step) to many, on any number of states, takes the
+ * same call.  Probabilities are rounded to the inputs' type for the product with v, as the
+ * score gradients are in the backward. */
+typedef struct {
+    oeq_dtype dtype;
+    int32_t n_struct;
+    int32_t n_heads, n_kv_heads, head_dim;
+    int64_t q_rows, k_rows;
+    int64_t q_stride, q_head_stride; /* elements from one row (head) to the next; the pointers */
+    int64_t k_stride, k_head_stride; /*   and the strides in bytes are multiples of 16, so a   */
+    int64_t v_stride, v_head_stride; /*   fused projection's q, k, v are taken in place        */
+    double scale;                    /* positive */
+    double p_drop;                   /* 0 <= p_drop < 1 */
+} oeq_attn_desc;
+
+/* Workspace bytes of the two directions (either pointer may be NULL). */
+oeq_status oeq_cross_attn_workspace_size(const oeq_attn_desc *desc, size_t *fwd_bytes,
+                                         size_t *bwd_bytes);
+
+/* out [q_rows, H, D] and lse [q_rows, H] (fp32, natural logarithm) are contiguous. */
+oeq_status oeq_cross_attn_fwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr,
+                              const void *q, const void *k, const void *v, const uint8_t *key_mask,
+                              const int64_t *rng, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Gradients of <grad_out, out>, from the forward's inputs, out and lse (the same p_drop and
+ * generator state): with P the dropped and scaled probabilities, dP = (grad_out v^T) keep /
+ * (1 - p') and delta = sum over D of grad_out out,
+ *   grad_v = P^T grad_out,  ds = p (dP - delta),  grad_q = scale ds k,  grad_k = scale ds^T q
+ * summed over the heads that share a key head.  grad_out, out and the gradients ([q_rows, H,
+ * D] and [k_rows, Hkv, D]) are contiguous and 16-byte aligned; any gradient may be NULL.
+ * States that are not visible get zero gradients. */
+oeq_status oeq_cross_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr,
+                              const void *q, const void *k, const void *v, const uint8_t *key_mask,
+                              const int64_t *rng, const void *out, const float *lse,
+                              const void *grad_out, void *grad_q, void *grad_k, void *grad_v,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronously validates a receiver CSR on the device (rowptr monotone,
  * rowptr[0] = 0, rowptr[N] = E, 0 <= src < N).  Test helper: synchronises. */
 oeq_status oeq_csr_check(int64_t n_nodes, int64_t n_edges, const int32_t *rowptr,
