@@ -23,7 +23,6 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liboeq.so")
 
 OEQ_F32, OEQ_F64, OEQ_F16, OEQ_BF16 = 0, 1, 2, 3
-ACTS = {"none": 0, "silu": 1}
 OEQ_BWD_ATOMIC, OEQ_BWD_DETERMINISTIC = 0, 1
 _MODES = {"atomic": OEQ_BWD_ATOMIC, "deterministic": OEQ_BWD_DETERMINISTIC}
 STATUS = {0: "OEQ_OK", 1: "OEQ_ERR_INVALID_ARG", 2: "OEQ_ERR_UNSUPPORTED", 3: "OEQ_ERR_WORKSPACE",
@@ -726,220 +725,17 @@ def oeq_tp_conv_bwd_radial(plan: Plan, rowptr, src, x, Y, vec, r_cut: float, W1,
 
 
 # ---------------------------------------------------------------------------
-# readout operators
+# readout operators (readout.py), loaded on first use: they need torch at import
 # ---------------------------------------------------------------------------
 
-def _elem(t, name):
-    """oeq_dtype of a readout operand."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    code = {torch.float32: OEQ_F32, torch.float16: OEQ_F16, torch.bfloat16: OEQ_BF16}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return code
+_READOUT = ("oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
+            "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd")
 
 
-def _rows(t, like, name):
-    """A 2-D operand whose rows may be strided (each row contiguous); returns its row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device != like.device:
-        raise TypeError(f"{name} must be a tensor on {like.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape) if like.dim() == 2 else '[rows, columns]'}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    if rows < 2:
-        return max(cols, 1)
-    if t.stride(0) < cols:
-        raise ValueError(f"the rows of {name} overlap")
-    return t.stride(0)
-
-
-def _scratch(nbytes, workspace, device):
-    """(tensor, bytes): the caller's workspace, or a 256-byte aligned one."""
-    import torch
-    if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    if nbytes == 0:
-        return None, 0
-    raw = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-    return raw[(-raw.data_ptr()) % 256:][:nbytes], nbytes
-
-
-def oeq_group_norm_workspace_size(n_rows: int, n_struct: int, n_channels: int, n_groups: int):
-    """Workspace bytes (forward, backward)."""
-    f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().oeq_group_norm_workspace_size(n_rows, n_struct, n_channels, n_groups, ctypes.byref(f),
-                                               ctypes.byref(b)))
-    return f.value, b.value
-
-
-def oeq_group_norm_fwd(x, ptr, n_groups: int, weight=None, bias=None, eps: float = 1e-5, act: str = "none", out=None,
-                       workspace=None):
-    """(out, mean, rstd): group norm of x [rows, C] over the rows of each structure
-    (ptr [structures + 1] int32), channels last, with an activation ("none" or "silu").
-    weight and bias are fp32 [C]; mean and rstd are fp32 [structures, n_groups]."""
-    import torch
-    code = _elem(x, "x")
-    ld = _rows(x, x, "x")
-    T, C = x.shape
-    B = ptr.shape[0] - 1
-    _want(ptr, (B + 1,), torch.int32, "ptr")
-    _want(weight, (C,), torch.float32, "weight")
-    _want(bias, (C,), torch.float32, "bias")
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    if out is None:
-        out = _empty((T, C), x.dtype, x.device)
-    ld_out = _rows(out, x, "out")
-    need = oeq_group_norm_workspace_size(T, B, C, n_groups)[0]
-    stats = _empty((2, B, n_groups), torch.float32, x.device)
-    mean, rstd = stats[0], stats[1]
-    ws, nbytes = _scratch(need, workspace, x.device)
-    _check(lib().oeq_group_norm_fwd(code, T, B, C, n_groups, ACTS[act], float(eps), _ptr(ptr), _ptr(x), ld,
-                                    _ptr(weight), _ptr(bias), _ptr(out), ld_out, _ptr(mean), _ptr(rstd), _ptr(ws),
-                                    nbytes, _stream()))
-    return out, mean, rstd
-
-
-def oeq_group_norm_bwd(x, ptr, n_groups: int, mean, rstd, grad_out, weight=None, bias=None, act: str = "none",
-                       need=("x", "weight", "bias"), out=None, workspace=None):
-    """(grad_x, grad_weight, grad_bias) of <grad_out, oeq_group_norm_fwd(x, ...)>; entries not in
-    `need` are None.  `out` may supply the grad_x tensor."""
-    import torch
-    code = _elem(x, "x")
-    ld = _rows(x, x, "x")
-    T, C = x.shape
-    B = ptr.shape[0] - 1
-    _want(ptr, (B + 1,), torch.int32, "ptr")
-    _want(weight, (C,), torch.float32, "weight")
-    _want(bias, (C,), torch.float32, "bias")
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    nbytes = oeq_group_norm_workspace_size(T, B, C, n_groups)[1]
-    _want(mean, (B, n_groups), torch.float32, "mean")
-    _want(rstd, (B, n_groups), torch.float32, "rstd")
-    ld_g = _rows(grad_out, x, "grad_out")
-    gx = None
-    if "x" in need:
-        gx = out if out is not None else _empty((T, C), x.dtype, x.device)
-    ld_gx = _rows(gx, x, "grad_x") if gx is not None else C
-    gw = _empty((C,), torch.float32, x.device) if "weight" in need else None
-    gb = _empty((C,), torch.float32, x.device) if "bias" in need else None
-    ws, nbytes = _scratch(nbytes, workspace, x.device)
-    _check(lib().oeq_group_norm_bwd(code, T, B, C, n_groups, ACTS[act], _ptr(ptr), _ptr(x), ld, _ptr(weight),
-                                    _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(grad_out), ld_g, _ptr(gx), ld_gx,
-                                    _ptr(gw), _ptr(gb), _ptr(ws), nbytes, _stream()))
-    return gx, gw, gb
-
-
-def oeq_dropout_fwd(x, p: float, rng, residual=None, out=None):
-    """residual + dropout(x) for x [rows, columns]; rng is an int64 device tensor (seed, offset)
-    read when the call runs.  The mask depends on rng and (row, column) only (see oeq.h).
-    `out` may be x or residual itself."""
-    import torch
-    code = _elem(x, "x")
-    ld = _rows(x, x, "x")
-    _want(rng, (2,), torch.int64, "rng")
-    ld_r = _rows(residual, x, "residual") if residual is not None else 0
-    if out is None:
-        out = _empty(x.shape, x.dtype, x.device)
-    ld_o = _rows(out, x, "out")
-    _check(lib().oeq_dropout_fwd(code, x.shape[0], x.shape[1], _ptr(x), ld, _ptr(residual), ld_r, float(p), _ptr(rng),
-                                 _ptr(out), ld_o, _stream()))
-    return out
-
-
-def oeq_dropout_bwd(grad_out, p: float, rng, out=None):
-    """Gradient to x of <grad_out, oeq_dropout_fwd(x, p, rng, ...)>."""
-    import torch
-    code = _elem(grad_out, "grad_out")
-    ld = _rows(grad_out, grad_out, "grad_out")
-    _want(rng, (2,), torch.int64, "rng")
-    if out is None:
-        out = _empty(grad_out.shape, grad_out.dtype, grad_out.device)
-    ld_o = _rows(out, grad_out, "grad_x")
-    _check(lib().oeq_dropout_bwd(code, grad_out.shape[0], grad_out.shape[1], _ptr(grad_out), ld, float(p), _ptr(rng),
-                                 _ptr(out), ld_o, _stream()))
-    return out
-
-
-def _heads(t, shape, like, name):
-    """A [rows, heads, dim] operand with strided rows and heads: its two strides."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device != like.device:
-        raise TypeError(f"{name} must be a tensor on {like.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    # the stride of a dimension of one is arbitrary: it is never stepped over
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
-
-
-def _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
-    import torch
-    code = _elem(q, "q")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be [rows, heads, dim]")
-    Tq, H, D = q.shape
-    Tk, Hk = k.shape[0], k.shape[1]
-    qs, ks, vs = _heads(q, (Tq, H, D), q, "q"), _heads(k, (Tk, Hk, D), q, "k"), _heads(v, (Tk, Hk, D), q, "v")
-    B = q_ptr.shape[0] - 1
-    _want(q_ptr, (B + 1,), torch.int32, "q_ptr")
-    _want(k_ptr, (B + 1,), torch.int32, "k_ptr")
-    if key_mask is not None:
-        _want(key_mask, (Tk,), torch.bool if key_mask.dtype == torch.bool else torch.uint8, "key_mask")
-    _want(rng, (2,), torch.int64, "rng")
-    return _AttnDesc(code, B, H, Hk, D, Tq, Tk, *qs, *ks, *vs, D ** -0.5 if scale is None else float(scale),
-                     float(p_drop))
-
-
-def oeq_cross_attn_fwd(q, k, v, q_ptr, k_ptr, scale=None, key_mask=None, p_drop: float = 0.0, rng=None, out=None,
-                       lse=None, workspace=None):
-    """(out, lse): attention of q [Tq, H, D] to the states k, v [Tk, Hkv, D] of their structure
-    (q_ptr, k_ptr: row pointers over the same structures).  scale defaults to 1 / sqrt(D);
-    key_mask [Tk] (bool or uint8) is nonzero where a state is visible; rng (see
-    oeq_dropout_fwd) is needed for p_drop > 0.  lse is fp32 [Tq, H]."""
-    import torch
-    d = _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
-    if out is None:
-        out = _empty(q.shape, q.dtype, q.device)
-    if lse is None:
-        lse = _empty(q.shape[:2], torch.float32, q.device)
-    _want(out, q.shape, q.dtype, "out")
-    _want(lse, q.shape[:2], torch.float32, "lse")
-    need = ctypes.c_size_t()
-    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), ctypes.byref(need), None))
-    ws, nbytes = _scratch(need.value, workspace, q.device)
-    _check(lib().oeq_cross_attn_fwd(ctypes.byref(d), _ptr(q_ptr), _ptr(k_ptr), _ptr(q), _ptr(k), _ptr(v),
-                                    _ptr(key_mask), _ptr(rng), _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream()))
-    return out, lse
-
-
-def oeq_cross_attn_bwd(q, k, v, q_ptr, k_ptr, out, lse, grad_out, scale=None, key_mask=None, p_drop: float = 0.0,
-                       rng=None, need=("q", "k", "v"), grads=None, workspace=None):
-    """(grad_q, grad_k, grad_v) of <grad_out, out> from the forward's operands, out and lse;
-    entries not in `need` are None.  `grads` may supply preallocated gradients."""
-    import torch
-    d = _attn_desc(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
-    _want(out, q.shape, q.dtype, "out")
-    _want(lse, q.shape[:2], torch.float32, "lse")
-    _want(grad_out, q.shape, q.dtype, "grad_out")
-    shapes = (q.shape, k.shape, k.shape)
-    if grads is None:
-        grads = tuple(_empty(s, q.dtype, q.device) if n in need else None for n, s in zip(("q", "k", "v"), shapes))
-    gq, gk, gv = (_want(t, s, q.dtype, "grad_" + n) for t, s, n in zip(grads, shapes, ("q", "k", "v")))
-    nb = ctypes.c_size_t()
-    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), None, ctypes.byref(nb)))
-    ws, nbytes = _scratch(nb.value, workspace, q.device)
-    _check(lib().oeq_cross_attn_bwd(ctypes.byref(d), _ptr(q_ptr), _ptr(k_ptr), _ptr(q), _ptr(k), _ptr(v),
-                                    _ptr(key_mask), _ptr(rng), _ptr(out), _ptr(lse), _ptr(grad_out), _ptr(gq),
-                                    _ptr(gk), _ptr(gv), _ptr(ws), nbytes, _stream()))
-    return gq, gk, gv
+def __getattr__(name):
+    if name not in _READOUT:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import readout
+    for n in _READOUT:
+        globals()[n] = getattr(readout, n)
+    return globals()[name]
