@@ -33,6 +33,8 @@ constexpr int kThreads = 256;
 constexpr int kSlab = 64;         // channels of a slab, where a group is not wider
 constexpr int kSplitRows = 256;   // rows a split has at least, on average
 constexpr int kMostSplits = 256;
+constexpr int kStep = 4;          // rows a thread has under way
+constexpr int kJoinChannels = 8;  // channels of a workgroup that sums the weights' gradients
 
 struct Shape {
     int cg;         // channels of a group
@@ -66,19 +68,29 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
+// Rows [begin, end) of a structure of `len` that split i of n has.
+struct Split {
+    int begin, end;
+};
+__device__ __forceinline__ Split split_of(int len, int i, int n) {
+    const int per = static_cast<int>((static_cast<unsigned>(len) + n - 1) / static_cast<unsigned>(n));
+    const int64_t at = int64_t(per) * i, next = at + per;
+    return {at < len ? static_cast<int>(at) : len, next < len ? static_cast<int>(next) : len};
+}
+
 // What a thread works on: the channels [c, c + n) (n <= 8, none for n <= 0) of the rows
-// begin + lane, begin + lane + lanes, ... of its split.
+// begin + lane, begin + lane + lanes, ..., `count` of them, of its split.
 struct Part {
     int64_t begin, end;
-    int c, n, lane, lanes, c0, width, g0, n_groups;
+    int c, n, lane, lanes, count, c0, width, g0, n_groups;
 };
 
 __device__ __forceinline__ Part part_of(const GroupNormArgs &a, const Shape &s, int b, int split, int slab) {
     Part p;
     const Span rows = span_of(a.ptr, b, a.rows);
-    const int64_t len = rows.end - rows.begin;
-    p.begin = rows.begin + len * split / s.splits;
-    p.end = rows.begin + len * (split + 1) / s.splits;
+    const Split in = split_of(static_cast<int>(rows.end - rows.begin), split, s.splits);
+    p.begin = rows.begin + in.begin;
+    p.end = rows.begin + in.end;
     p.g0 = slab * s.gps;
     p.n_groups = a.groups - p.g0 < s.gps ? a.groups - p.g0 : s.gps;
     p.c0 = p.g0 * s.cg;
@@ -88,33 +100,76 @@ __device__ __forceinline__ Part part_of(const GroupNormArgs &a, const Shape &s, 
     p.n = p.width - col * 8 < 8 ? p.width - col * 8 : 8;
     p.lane = threadIdx.x / s.cols;
     p.lanes = kThreads / s.cols;
+    p.count = p.n > 0 ? (static_cast<int>(p.end - p.begin) - p.lane + p.lanes - 1) / p.lanes : 0;
     return p;
 }
 
-template <class T>
-__device__ __forceinline__ f32x8 fetch(const void *base, int64_t ld, int64_t row, const Part &p) {
-    const T *at = static_cast<const T *>(base) + row * ld + p.c;
-    return to_f32<T>(p.n == 8 ? load8(at) : load_part(at, p.n));
-}
-template <class T>
-__device__ __forceinline__ void put(void *base, int64_t ld, int64_t row, const Part &p, f32x8 v) {
-    T *at = static_cast<T *>(base) + row * ld + p.c;
-    const vec8<T> o = from_f32<T>(v);
-    if (p.n == 8)
-        store8(at, o);
-    else
-        store_part(at, o, p.n);
-}
+// A thread's rows of one operand, kStep at a time.  kFull: every piece has all eight channels.
+template <class T, bool kFull>
+struct Walk {
+    T *at;
+    int64_t stride;
+    int n;
+    __device__ __forceinline__ Walk(const void *base, int64_t ld, const Part &p)
+        : at(static_cast<T *>(const_cast<void *>(base)) + (p.begin + p.lane) * ld + p.c), stride(p.lanes * ld), n(p.n) {}
+    // All loads of a step are issued together; in place of rows past the `left` ones the first is
+    // read, and its value not used.
+    __device__ __forceinline__ void load(vec8<T> (&v)[kStep], int left) const {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const T *q = at + (i < left ? i * stride : 0);
+            v[i] = kFull || n == 8 ? load8(q) : load_part(q, n);
+        }
+    }
+    __device__ __forceinline__ void store(int i, f32x8 v) const {
+        T *q = at + i * stride;
+        const vec8<T> o = from_f32<T>(v);
+        if (kFull || n == 8)
+            store8(q, o);
+        else
+            store_part(q, o, n);
+    }
+    __device__ __forceinline__ void next() { at += kStep * stride; }
+};
+
 __device__ __forceinline__ f32x8 channel_values(const float *v, const Part &p, float without) {
     f32x8 o;
+    if (v && p.n == 8) return load8(v + p.c);
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = v && j < p.n ? v[p.c + j] : without;
     return o;
 }
 
-// Sums two values per channel over the rows' threads; afterwards sums[i][c - c0] holds them.
-// `sums` has room for kThreads * 8 values a piece.
-__device__ __forceinline__ void channel_sums(f32x8 u, f32x8 v, const Part &p, int cols, float (*sums)[kThreads * 8]) {
+// f(j, group) for the thread's channels; channel c is the first of them, counted from the
+// first channel of the first group.
+template <class F>
+__device__ __forceinline__ void each_group(const Part &p, const Shape &s, int c, F &&f) {
+    if (p.n <= 0) return;
+    int g = c / s.cg, in = c - g * s.cg;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j < p.n) f(j, g);
+        if (++in == s.cg) {
+            in = 0;
+            ++g;
+        }
+    }
+}
+
+// Two sums per channel of all threads' rows: every thread leaves its own with those of the
+// other row lanes of its wave, by set of waves that hold the same channels; channel_total
+// adds the sets.
+struct Sums {
+    float v[2][kThreads * 8];
+    float shift[kThreads * 8];  // the first row (statistics)
+    int cols, sets;
+    __device__ __forceinline__ double total(int which, int c) const {
+        double t = v[which][c];
+        for (int k = 1; k < sets; ++k) t += v[which][k * cols * 8 + c];
+        return t;
+    }
+};
+__device__ __forceinline__ void channel_sums(f32x8 u, f32x8 v, const Part &p, int cols, Sums &sums) {
     for (int off = cols; off < 64; off <<= 1) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -122,124 +177,166 @@ __device__ __forceinline__ void channel_sums(f32x8 u, f32x8 v, const Part &p, in
             v[j] += __shfl_xor(v[j], off);
         }
     }
-    // waves that hold the same channels are added in order through LDS
-    const int per_set = cols > 64 ? cols / 64 : 1, sets = 4 / per_set, wave = threadIdx.x >> 6;
+    const int per_set = cols > 64 ? cols / 64 : 1, wave = threadIdx.x >> 6;
     const int col = threadIdx.x & (cols - 1), set = wave / per_set;
     if (p.lane % (cols < 64 ? 64 / cols : 1) == 0 && p.n > 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            sums[0][set * cols * 8 + col * 8 + j] = u[j];
-            sums[1][set * cols * 8 + col * 8 + j] = v[j];
+            sums.v[0][set * cols * 8 + col * 8 + j] = u[j];
+            sums.v[1][set * cols * 8 + col * 8 + j] = v[j];
         }
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.width; c += kThreads) {
-        for (int k = 1; k < sets; ++k) {
-            sums[0][c] += sums[0][k * cols * 8 + c];
-            sums[1][c] += sums[1][k * cols * 8 + c];
-        }
+    if (threadIdx.x == 0) {
+        sums.cols = cols;
+        sums.sets = kThreads / 64 / per_set;
     }
     __syncthreads();
 }
 
-// Mean and sum of squared deviations of each group of the slab over the part's rows, left in
-// group_mean / group_m2 (LDS, by group of the slab).
-template <class T>
-__device__ __forceinline__ void statistics(const GroupNormArgs &a, const Shape &s, const Part &p,
-                                           float (*sums)[kThreads * 8], double *group_mean, double *group_m2) {
+// Groups of the slab, several a wave: `group` is -1 for lanes without one, `lane` the lane
+// within the group's `lanes` (a power of two), which step through its channels.
+struct GroupLanes {
+    int lanes, lane, at;
+    __device__ __forceinline__ explicit GroupLanes(int cg) {
+        lanes = 1;
+        while (lanes < cg && lanes < 64) lanes <<= 1;
+        lane = threadIdx.x & (lanes - 1);
+        at = threadIdx.x / lanes;
+    }
+    __device__ __forceinline__ int step() const { return kThreads / lanes; }
+    __device__ __forceinline__ double sum(double v) const {
+        for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor(v, off);
+        return v;
+    }
+};
+
+__device__ __forceinline__ float rstd_of(double m2, double n, float eps) {
+    if (!(n > 0)) return 0.f;
+    const double var = m2 > 0 || !(m2 == m2) ? m2 / n : 0;  // rounding can leave a small negative sum
+    const float v = static_cast<float>(var + double(eps)), r = __builtin_amdgcn_rsqf(v);
+    return v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;  // a Newton step; rsq(inf) is 0 already
+}
+
+// Statistics of each group of the slab over the part's rows; emit(group of the slab, mean, sum
+// of squared deviations) is called by one lane for each.  The part's first rows stay in `held`.
+template <class T, bool kFull, class Emit>
+__device__ __forceinline__ void statistics(const GroupNormArgs &a, const Shape &s, const Part &p, vec8<T> (&held)[kStep],
+                                           Sums &sums, Emit &&emit) {
     const int64_t n = p.end - p.begin;
-    f32x8 shift = {}, u = {}, v = {};
-    if (p.n > 0 && n > 0) {
-        shift = fetch<T>(a.x, a.ld_x, p.begin, p);
-#pragma unroll 4
-        for (int64_t r = p.begin + p.lane; r < p.end; r += p.lanes) {
-            const f32x8 d = fetch<T>(a.x, a.ld_x, r, p) - shift;
-            u += d;
-            v += d * d;
+    f32x8 u = {}, v = {};
+    if (p.count > 0) {
+        Walk<T, kFull> x(a.x, a.ld_x, p);
+        x.load(held, p.count);
+        const T *first = static_cast<const T *>(a.x) + p.begin * a.ld_x + p.c;
+        const f32x8 shift = to_f32<T>(kFull || p.n == 8 ? load8(first) : load_part(first, p.n));
+        const auto add = [&](const vec8<T>(&rows)[kStep], int left) {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                if (i < left) {
+                    const f32x8 d = to_f32<T>(rows[i]) - shift;
+                    u += d;
+                    v += d * d;
+                }
+            }
+        };
+        if (p.lane == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sums.shift[p.c - p.c0 + j] = shift[j];
+        }
+        add(held, p.count);
+        for (int left = p.count - kStep; left > 0; left -= kStep) {
+            vec8<T> rows[kStep];
+            x.next();
+            x.load(rows, left);
+            add(rows, left);
         }
     }
     channel_sums(u, v, p, s.cols, sums);
-    const int lane = threadIdx.x & 63;
-    for (int g = threadIdx.x >> 6; g < p.n_groups; g += kThreads / 64) {
+    const GroupLanes gl(s.cg);
+    for (int g = gl.at; g < (p.n_groups + gl.step() - 1) / gl.step() * gl.step(); g += gl.step()) {
         double mean = 0, m2 = 0;
-        if (n > 0) {
-            const T *first = static_cast<const T *>(a.x) + p.begin * a.ld_x + p.c0 + g * s.cg;
-            for (int c = lane; c < s.cg; c += 64)
-                mean += double(static_cast<float>(first[c])) + double(sums[0][g * s.cg + c]) / double(n);
-            mean = wave_sum(mean) / s.cg;
-            for (int c = lane; c < s.cg; c += 64) {
-                const double total = sums[0][g * s.cg + c];
-                const double off = double(static_cast<float>(first[c])) + total / double(n) - mean;
-                const double own = double(sums[1][g * s.cg + c]) - total * total / double(n);
-                m2 += own + double(n) * off * off;
+        if (g < p.n_groups && n > 0) {
+            const float *first = sums.shift + g * s.cg;
+            const double inv = 1.0 / double(n);
+            for (int c = gl.lane; c < s.cg; c += gl.lanes)
+                mean += double(first[c]) + sums.total(0, g * s.cg + c) * inv;
+            mean = gl.sum(mean) / s.cg;
+            for (int c = gl.lane; c < s.cg; c += gl.lanes) {
+                const double total = sums.total(0, g * s.cg + c);
+                const double off = double(first[c]) + total * inv - mean;
+                m2 += sums.total(1, g * s.cg + c) - total * total * inv + double(n) * off * off;
             }
-            m2 = wave_sum(m2);
+            m2 = gl.sum(m2);
         }
-        if (lane == 0) {
-            group_mean[g] = mean;
-            group_m2[g] = m2;
-        }
+        if (gl.lane == 0 && g < p.n_groups) emit(g, mean, m2);
     }
-    __syncthreads();
 }
 
-__device__ __forceinline__ float rstd_of(double m2, double n, float eps) {
-    const double var = m2 > 0 || !(m2 == m2) ? m2 / n : 0;  // rounding can leave a small negative sum
-    return n > 0 ? static_cast<float>(1.0 / sqrt(var + double(eps))) : 0.f;
-}
-
-template <class T, bool kSilu>
-__device__ __forceinline__ void apply_forward(const GroupNormArgs &a, const Part &p, f32x8 mean, f32x8 rstd) {
-    if (p.n <= 0) return;
-    const f32x8 w = channel_values(a.weight, p, 1.f) * rstd, bias = channel_values(a.bias, p, 0.f);
-#pragma unroll 4
-    for (int64_t r = p.begin + p.lane; r < p.end; r += p.lanes) {
-        f32x8 z = (fetch<T>(a.x, a.ld_x, r, p) - mean) * w + bias;
-        if (kSilu) {
+// out of a part's rows; the first are in `held`.
+template <class T, bool kFull, bool kSilu>
+__device__ __forceinline__ void apply_forward(const GroupNormArgs &a, const Part &p, const vec8<T> (&held)[kStep],
+                                              f32x8 mean, f32x8 w, f32x8 bias) {
+    if (p.count <= 0) return;
+    Walk<T, kFull> x(a.x, a.ld_x, p), out(a.out, a.ld_out, p);
+    const auto apply = [&](const vec8<T>(&rows)[kStep], int left) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] *= sigmoid(z[j]);
+        for (int i = 0; i < kStep; ++i) {
+            if (i < left) {
+                f32x8 z = (to_f32<T>(rows[i]) - mean) * w + bias;
+                if (kSilu) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] *= sigmoid(z[j]);
+                }
+                out.store(i, z);
+            }
         }
-        put<T>(a.out, a.ld_out, r, p, z);
+    };
+    apply(held, p.count);
+    for (int left = p.count - kStep; left > 0; left -= kStep) {
+        vec8<T> rows[kStep];
+        x.next();
+        out.next();
+        x.load(rows, left);
+        apply(rows, left);
     }
 }
 
 // One split: statistics and output in one launch.
-template <class T, bool kSilu>
+template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_forward(GroupNormArgs a, Shape s) {
-    __shared__ float sums[2][kThreads * 8];
-    __shared__ double group_mean[kSlab], group_m2[kSlab];
+    __shared__ Sums sums;
+    __shared__ float group_mean[kSlab], group_rstd[kSlab];
     const int b = blockIdx.x / s.n_slabs;
-    const Part p = part_of(a, s, b, 0, blockIdx.x % s.n_slabs);
-    statistics<T>(a, s, p, sums, group_mean, group_m2);
+    const Part p = part_of(a, s, b, 0, blockIdx.x - b * s.n_slabs);
+    f32x8 w = channel_values(a.weight, p, 1.f), bias = channel_values(a.bias, p, 0.f), mean = {};
+    vec8<T> held[kStep];
     const double n = double(p.end - p.begin) * s.cg;
-    f32x8 mean = {}, rstd = {};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j < p.n) {
-            const int g = (p.c + j - p.c0) / s.cg;
-            mean[j] = static_cast<float>(group_mean[g]);
-            rstd[j] = rstd_of(group_m2[g], n, a.eps);
-        }
-    }
-    if (threadIdx.x < p.n_groups) {
-        const int64_t at = int64_t(b) * a.groups + p.g0 + threadIdx.x;
-        a.mean[at] = static_cast<float>(group_mean[threadIdx.x]);
-        a.rstd[at] = rstd_of(group_m2[threadIdx.x], n, a.eps);
-    }
-    apply_forward<T, kSilu>(a, p, mean, rstd);
+    statistics<T, kFull>(a, s, p, held, sums, [&](int g, double group, double m2) {
+        const float rstd = rstd_of(m2, n, a.eps);
+        group_mean[g] = static_cast<float>(group);
+        group_rstd[g] = rstd;
+        const int64_t at = int64_t(b) * a.groups + p.g0 + g;
+        a.mean[at] = static_cast<float>(group);
+        a.rstd[at] = rstd;
+    });
+    __syncthreads();
+    each_group(p, s, p.c - p.c0, [&](int j, int g) {
+        mean[j] = group_mean[g];
+        w[j] *= group_rstd[g];
+    });
+    apply_forward<T, kFull, kSilu>(a, p, held, mean, w, bias);
 }
 
 // Several splits.  partial[(b, split, group)] = {mean, sum of squared deviations}
-template <class T>
+template <class T, bool kFull>
 __global__ void __launch_bounds__(kThreads) k_statistics(GroupNormArgs a, Shape s, double2 *partial) {
-    __shared__ float sums[2][kThreads * 8];
-    __shared__ double group_mean[kSlab], group_m2[kSlab];
-    const int64_t part = blockIdx.x / s.n_slabs;
-    const Part p = part_of(a, s, static_cast<int>(part / s.splits), static_cast<int>(part % s.splits),
-                           blockIdx.x % s.n_slabs);
-    statistics<T>(a, s, p, sums, group_mean, group_m2);
-    if (threadIdx.x < p.n_groups)
-        partial[part * a.groups + p.g0 + threadIdx.x] = make_double2(group_mean[threadIdx.x], group_m2[threadIdx.x]);
+    __shared__ Sums sums;
+    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    vec8<T> held[kStep];
+    statistics<T, kFull>(a, s, p, held, sums, [&](int g, double mean, double m2) {
+        partial[int64_t(part) * a.groups + p.g0 + g] = make_double2(mean, m2);
+    });
 }
 
 // One wave joins the splits of one (structure, group).
@@ -248,19 +345,26 @@ __global__ void __launch_bounds__(kThreads) k_join_statistics(GroupNormArgs a, S
     if (at >= int64_t(a.n_struct) * a.groups) return;
     const int b = static_cast<int>(at / a.groups), g = static_cast<int>(at % a.groups), lane = threadIdx.x & 63;
     const Span rows = span_of(a.ptr, b, a.rows);
-    const int64_t len = rows.end - rows.begin;
+    const int len = static_cast<int>(rows.end - rows.begin);
     const double n = double(len) * s.cg;
-    double mean = 0, m2 = 0;
-    for (int i = lane; i < s.splits; i += 64) {
-        const double k = double(len * (i + 1) / s.splits - len * i / s.splits) * s.cg;
-        mean += k * partial[(int64_t(b) * s.splits + i) * a.groups + g].x;
+    constexpr int kMine = kMostSplits / 64;
+    double2 v[kMine];
+    double k[kMine], mean = 0, m2 = 0;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = lane + 64 * j;
+        v[j] = i < s.splits ? partial[(int64_t(b) * s.splits + i) * a.groups + g] : make_double2(0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const Split in = split_of(len, lane + 64 * j, s.splits);
+        k[j] = double(in.end - in.begin) * s.cg;
+        if (k[j] > 0) mean += k[j] * v[j].x;
     }
     mean = n > 0 ? wave_sum(mean) / n : 0;
-    for (int i = lane; i < s.splits; i += 64) {
-        const double k = double(len * (i + 1) / s.splits - len * i / s.splits) * s.cg;
-        const double2 v = partial[(int64_t(b) * s.splits + i) * a.groups + g];
-        if (k > 0) m2 += v.y + k * (v.x - mean) * (v.x - mean);
-    }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+        if (k[j] > 0) m2 += v[j].y + k[j] * (v[j].x - mean) * (v[j].x - mean);
     m2 = wave_sum(m2);
     if (lane == 0) {
         a.mean[at] = static_cast<float>(mean);
@@ -272,140 +376,183 @@ __device__ __forceinline__ void saved_statistics(const GroupNormArgs &a, const S
                                                  f32x8 *mean, f32x8 *rstd) {
     *mean = f32x8{};
     *rstd = f32x8{};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j < p.n) {
-            const int64_t at = int64_t(b) * a.groups + (p.c + j) / s.cg;
-            (*mean)[j] = a.mean[at];
-            (*rstd)[j] = a.rstd[at];
-        }
-    }
+    each_group(p, s, p.c, [&](int j, int g) {
+        const int64_t at = int64_t(b) * a.groups + g;
+        (*mean)[j] = a.mean[at];
+        (*rstd)[j] = a.rstd[at];
+    });
 }
 
-template <class T, bool kSilu>
+template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply(GroupNormArgs a, Shape s) {
-    const int64_t part = blockIdx.x / s.n_slabs;
-    const int b = static_cast<int>(part / s.splits);
-    const Part p = part_of(a, s, b, static_cast<int>(part % s.splits), blockIdx.x % s.n_slabs);
+    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
     f32x8 mean, rstd;
+    vec8<T> held[kStep];
+    if (p.count > 0) Walk<T, kFull>(a.x, a.ld_x, p).load(held, p.count);
     saved_statistics(a, s, b, p, &mean, &rstd);
-    apply_forward<T, kSilu>(a, p, mean, rstd);
+    const f32x8 w = channel_values(a.weight, p, 1.f) * rstd, bias = channel_values(a.bias, p, 0.f);
+    apply_forward<T, kFull, kSilu>(a, p, held, mean, w, bias);
 }
 
 // ---- backward -----------------------------------------------------------------------
 
-// xhat and dz of eight elements
-template <class T, bool kSilu>
-__device__ __forceinline__ void local_gradient(const GroupNormArgs &a, int64_t r, const Part &p, f32x8 mean, f32x8 rstd,
-                                               f32x8 w, f32x8 bias, f32x8 *xhat, f32x8 *dz) {
-    const f32x8 h = (fetch<T>(a.x, a.ld_x, r, p) - mean) * rstd;
-    f32x8 g = fetch<T>(a.grad_out, a.ld_grad_out, r, p);
-    if (kSilu) {
-        const f32x8 z = h * w + bias;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float gate = sigmoid(z[j]);
-            g[j] *= gate * (1.f + z[j] * (1.f - gate));
-        }
+// What a thread needs of its channels; z = (x - mean) scale + bias with scale = rstd w.
+struct Channels {
+    f32x8 mean, rstd, scale, bias;
+    __device__ __forceinline__ Channels(const GroupNormArgs &a, const Shape &s, int b, const Part &p) {
+        saved_statistics(a, s, b, p, &mean, &rstd);
+        scale = channel_values(a.weight, p, 1.f) * rstd;
+        bias = channel_values(a.bias, p, 0.f);
     }
-    *xhat = h;
-    *dz = g;
-}
+    // x - mean and dz of one row
+    template <class T, bool kSilu>
+    __device__ __forceinline__ void local(vec8<T> x, vec8<T> g, f32x8 *centred, f32x8 *dz) const {
+        const f32x8 xc = to_f32<T>(x) - mean;
+        f32x8 d = to_f32<T>(g);
+        if (kSilu) {
+            const f32x8 z = xc * scale + bias;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float gate = sigmoid(z[j]);
+                d[j] *= fmaf(z[j] * gate, 1.f - gate, gate);
+            }
+        }
+        *centred = xc;
+        *dz = d;
+    }
+};
 
 // Sums of a part's dz and dz xhat by channel (to `column`, unless NULL: row `part` of two
-// fp32 rows of C channels) and, weighted, by group of the slab (left in LDS).
-template <class T, bool kSilu>
+// fp32 rows of C channels) and, weighted, by group (to emit, as in statistics).  The part's
+// first rows stay in hx and hg.
+template <class T, bool kFull, bool kSilu, class Emit>
 __device__ __forceinline__ void gradient_sums(const GroupNormArgs &a, const Shape &s, const Part &p, int64_t part,
-                                              f32x8 mean, f32x8 rstd, f32x8 w, f32x8 bias, float *column,
-                                              float (*sums)[kThreads * 8], double *group_dh, double *group_dhx) {
+                                              const Channels &ch, vec8<T> (&hx)[kStep], vec8<T> (&hg)[kStep],
+                                              float *column, Sums &sums, Emit &&emit) {
     f32x8 u = {}, v = {};
-    if (p.n > 0) {
-#pragma unroll 2
-        for (int64_t r = p.begin + p.lane; r < p.end; r += p.lanes) {
-            f32x8 xhat, dz;
-            local_gradient<T, kSilu>(a, r, p, mean, rstd, w, bias, &xhat, &dz);
-            u += dz;
-            v += dz * xhat;
+    if (p.count > 0) {
+        Walk<T, kFull> x(a.x, a.ld_x, p), g(a.grad_out, a.ld_grad_out, p);
+        const auto add = [&](const vec8<T>(&rx)[kStep], const vec8<T>(&rg)[kStep], int left) {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                if (i < left) {
+                    f32x8 xc, dz;
+                    ch.local<T, kSilu>(rx[i], rg[i], &xc, &dz);
+                    u += dz;
+                    v += dz * xc;
+                }
+            }
+        };
+        add(hx, hg, p.count);
+        for (int left = p.count - kStep; left > 0; left -= kStep) {
+            vec8<T> rx[kStep], rg[kStep];
+            x.next();
+            g.next();
+            x.load(rx, left);
+            g.load(rg, left);
+            add(rx, rg, left);
         }
+        v *= ch.rstd;
     }
     channel_sums(u, v, p, s.cols, sums);
     if (column) {
         for (int c = threadIdx.x; c < p.width; c += kThreads) {
-            column[part * 2 * a.channels + p.c0 + c] = sums[0][c];
-            column[(part * 2 + 1) * a.channels + p.c0 + c] = sums[1][c];
+            column[part * 2 * a.channels + p.c0 + c] = static_cast<float>(sums.total(0, c));
+            column[(part * 2 + 1) * a.channels + p.c0 + c] = static_cast<float>(sums.total(1, c));
         }
     }
-    const int lane = threadIdx.x & 63;
-    for (int g = threadIdx.x >> 6; g < p.n_groups; g += kThreads / 64) {
+    const GroupLanes gl(s.cg);
+    for (int g = gl.at; g < (p.n_groups + gl.step() - 1) / gl.step() * gl.step(); g += gl.step()) {
         double dh = 0, dhx = 0;
-        for (int c = lane; c < s.cg; c += 64) {
-            const double wc = a.weight ? a.weight[p.c0 + g * s.cg + c] : 1.f;
-            dh += wc * sums[0][g * s.cg + c];
-            dhx += wc * sums[1][g * s.cg + c];
+        if (g < p.n_groups) {
+            for (int c = gl.lane; c < s.cg; c += gl.lanes) {
+                const double wc = a.weight ? a.weight[p.c0 + g * s.cg + c] : 1.f;
+                dh += wc * sums.total(0, g * s.cg + c);
+                dhx += wc * sums.total(1, g * s.cg + c);
+            }
+            dh = gl.sum(dh);
+            dhx = gl.sum(dhx);
         }
-        dh = wave_sum(dh);
-        dhx = wave_sum(dhx);
-        if (lane == 0) {
-            group_dh[g] = dh;
-            group_dhx[g] = dhx;
-        }
-    }
-    __syncthreads();
-}
-
-template <class T, bool kSilu>
-__device__ __forceinline__ void apply_backward(const GroupNormArgs &a, const Part &p, f32x8 mean, f32x8 rstd, f32x8 w,
-                                               f32x8 bias, f32x8 m1, f32x8 m2) {
-    if (p.n <= 0) return;
-#pragma unroll 2
-    for (int64_t r = p.begin + p.lane; r < p.end; r += p.lanes) {
-        f32x8 xhat, dz;
-        local_gradient<T, kSilu>(a, r, p, mean, rstd, w, bias, &xhat, &dz);
-        put<T>(a.grad_x, a.ld_grad_x, r, p, rstd * (dz * w - m1 - xhat * m2));
+        if (gl.lane == 0 && g < p.n_groups) emit(g, dh, dhx);
     }
 }
 
-template <class T, bool kSilu>
-__global__ void __launch_bounds__(kThreads) k_backward(GroupNormArgs a, Shape s, float *column) {
-    __shared__ float sums[2][kThreads * 8];
-    __shared__ double group_dh[kSlab], group_dhx[kSlab];
-    const int b = blockIdx.x / s.n_slabs;
-    const Part p = part_of(a, s, b, 0, blockIdx.x % s.n_slabs);
-    f32x8 mean, rstd;
-    saved_statistics(a, s, b, p, &mean, &rstd);
-    const f32x8 w = channel_values(a.weight, p, 1.f), bias = channel_values(a.bias, p, 0.f);
-    gradient_sums<T, kSilu>(a, s, p, b, mean, rstd, w, bias, column, sums, group_dh, group_dhx);
-    if (!a.grad_x) return;
-    const double n = double(p.end - p.begin) * s.cg;
-    f32x8 m1 = {}, m2 = {};
+// grad_x = scale dz - rstd m1 - (x - mean) rstd^2 m2
+template <class T, bool kFull, bool kSilu>
+__device__ __forceinline__ void apply_backward(const GroupNormArgs &a, const Part &p, const Channels &ch,
+                                               const vec8<T> (&hx)[kStep], const vec8<T> (&hg)[kStep], f32x8 m1, f32x8 m2) {
+    if (p.count <= 0) return;
+    Walk<T, kFull> x(a.x, a.ld_x, p), g(a.grad_out, a.ld_grad_out, p), out(a.grad_x, a.ld_grad_x, p);
+    const f32x8 k1 = ch.rstd * m1, k2 = ch.rstd * ch.rstd * m2;
+    const auto apply = [&](const vec8<T>(&rx)[kStep], const vec8<T>(&rg)[kStep], int left) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j < p.n && n > 0) {
-            const int g = (p.c + j - p.c0) / s.cg;
-            m1[j] = static_cast<float>(group_dh[g] / n);
-            m2[j] = static_cast<float>(group_dhx[g] / n);
+        for (int i = 0; i < kStep; ++i) {
+            if (i < left) {
+                f32x8 xc, dz;
+                ch.local<T, kSilu>(rx[i], rg[i], &xc, &dz);
+                out.store(i, dz * ch.scale - k1 - xc * k2);
+            }
         }
+    };
+    apply(hx, hg, p.count);
+    for (int left = p.count - kStep; left > 0; left -= kStep) {
+        vec8<T> rx[kStep], rg[kStep];
+        x.next();
+        g.next();
+        out.next();
+        x.load(rx, left);
+        g.load(rg, left);
+        apply(rx, rg, left);
     }
-    apply_backward<T, kSilu>(a, p, mean, rstd, w, bias, m1, m2);
 }
 
-template <class T, bool kSilu>
+template <class T, bool kFull>
+__device__ __forceinline__ void hold(const GroupNormArgs &a, const Part &p, vec8<T> (&hx)[kStep], vec8<T> (&hg)[kStep]) {
+    if (p.count <= 0) return;
+    Walk<T, kFull>(a.x, a.ld_x, p).load(hx, p.count);
+    Walk<T, kFull>(a.grad_out, a.ld_grad_out, p).load(hg, p.count);
+}
+
+template <class T, bool kFull, bool kSilu>
+__global__ void __launch_bounds__(kThreads) k_backward(GroupNormArgs a, Shape s, float *column) {
+    __shared__ Sums sums;
+    __shared__ float group_m1[kSlab], group_m2[kSlab];
+    const int b = blockIdx.x / s.n_slabs;
+    const Part p = part_of(a, s, b, 0, blockIdx.x - b * s.n_slabs);
+    vec8<T> hx[kStep], hg[kStep];
+    hold<T, kFull>(a, p, hx, hg);
+    const Channels ch(a, s, b, p);
+    const double n = double(p.end - p.begin) * s.cg;
+    gradient_sums<T, kFull, kSilu>(a, s, p, b, ch, hx, hg, column, sums, [&](int g, double dh, double dhx) {
+        group_m1[g] = n > 0 ? static_cast<float>(dh / n) : 0.f;
+        group_m2[g] = n > 0 ? static_cast<float>(dhx / n) : 0.f;
+    });
+    if (!a.grad_x) return;
+    __syncthreads();
+    f32x8 m1 = {}, m2 = {};
+    each_group(p, s, p.c - p.c0, [&](int j, int g) {
+        m1[j] = group_m1[g];
+        m2[j] = group_m2[g];
+    });
+    apply_backward<T, kFull, kSilu>(a, p, ch, hx, hg, m1, m2);
+}
+
+template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_gradient_sums(GroupNormArgs a, Shape s, float *column, double2 *partial) {
-    __shared__ float sums[2][kThreads * 8];
-    __shared__ double group_dh[kSlab], group_dhx[kSlab];
-    const int64_t part = blockIdx.x / s.n_slabs;
-    const int b = static_cast<int>(part / s.splits);
-    const Part p = part_of(a, s, b, static_cast<int>(part % s.splits), blockIdx.x % s.n_slabs);
-    f32x8 mean, rstd;
-    saved_statistics(a, s, b, p, &mean, &rstd);
-    const f32x8 w = channel_values(a.weight, p, 1.f), bias = channel_values(a.bias, p, 0.f);
-    gradient_sums<T, kSilu>(a, s, p, part, mean, rstd, w, bias, column, sums, group_dh, group_dhx);
-    if (threadIdx.x < p.n_groups)
-        partial[part * a.groups + p.g0 + threadIdx.x] = make_double2(group_dh[threadIdx.x], group_dhx[threadIdx.x]);
+    __shared__ Sums sums;
+    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    vec8<T> hx[kStep], hg[kStep];
+    hold<T, kFull>(a, p, hx, hg);
+    const Channels ch(a, s, b, p);
+    gradient_sums<T, kFull, kSilu>(a, s, p, part, ch, hx, hg, column, sums, [&](int g, double dh, double dhx) {
+        partial[int64_t(part) * a.groups + p.g0 + g] = make_double2(dh, dhx);
+    });
 }
 
 // The first `join_blocks` workgroups join the splits' group sums to means (one wave a
-// (structure, group)); the others sum `column` over its rows, 16 channels a workgroup.
+// (structure, group)); the others sum `column` over its rows, kJoinChannels a workgroup.
 __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Shape s, const double2 *partial,
                                                              float2 *joined, const float *column, int join_blocks) {
     if (static_cast<int>(blockIdx.x) < join_blocks) {
@@ -427,46 +574,56 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
         return;
     }
     __shared__ double part[2][kThreads];
-    const int c = (blockIdx.x - join_blocks) * 16 + (threadIdx.x & 15), lane = threadIdx.x >> 4;
-    const int64_t n_parts = int64_t(a.n_struct) * s.splits;
+    constexpr int kLanes = kThreads / kJoinChannels, kAhead = 8;
+    const int col = threadIdx.x % kJoinChannels, lane = threadIdx.x / kJoinChannels;
+    const int c = (blockIdx.x - join_blocks) * kJoinChannels + col;
+    const int n_parts = a.n_struct * s.splits;
     double u = 0, v = 0;
     if (c < a.channels) {
-#pragma unroll 4
-        for (int64_t r = lane; r < n_parts; r += kThreads / 16) {
-            u += column[r * 2 * a.channels + c];
-            v += column[(r * 2 + 1) * a.channels + c];
+        for (int r = lane; r < n_parts; r += kLanes * kAhead) {
+            float x[kAhead], y[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t at = r + i * kLanes < n_parts ? r + i * kLanes : r;
+                x[i] = column[at * 2 * a.channels + c];
+                y[i] = column[(at * 2 + 1) * a.channels + c];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (r + i * kLanes < n_parts) {
+                    u += x[i];
+                    v += y[i];
+                }
+            }
         }
     }
     part[0][threadIdx.x] = u;
     part[1][threadIdx.x] = v;
     __syncthreads();
-    if (threadIdx.x < 16 && c < a.channels) {
-        for (int k = 1; k < kThreads / 16; ++k) {
-            u += part[0][k * 16 + threadIdx.x];
-            v += part[1][k * 16 + threadIdx.x];
+    if (threadIdx.x < kJoinChannels && c < a.channels) {
+        for (int k = 1; k < kLanes; ++k) {
+            u += part[0][k * kJoinChannels + col];
+            v += part[1][k * kJoinChannels + col];
         }
         if (a.grad_bias) a.grad_bias[c] = static_cast<float>(u);
         if (a.grad_weight) a.grad_weight[c] = static_cast<float>(v);
     }
 }
 
-template <class T, bool kSilu>
+template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply_backward(GroupNormArgs a, Shape s, const float2 *joined) {
-    const int64_t part = blockIdx.x / s.n_slabs;
-    const int b = static_cast<int>(part / s.splits);
-    const Part p = part_of(a, s, b, static_cast<int>(part % s.splits), blockIdx.x % s.n_slabs);
-    f32x8 mean, rstd, m1 = {}, m2 = {};
-    saved_statistics(a, s, b, p, &mean, &rstd);
-    const f32x8 w = channel_values(a.weight, p, 1.f), bias = channel_values(a.bias, p, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j < p.n) {
-            const float2 t = joined[int64_t(b) * a.groups + (p.c + j) / s.cg];
-            m1[j] = t.x;
-            m2[j] = t.y;
-        }
-    }
-    apply_backward<T, kSilu>(a, p, mean, rstd, w, bias, m1, m2);
+    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    vec8<T> hx[kStep], hg[kStep];
+    hold<T, kFull>(a, p, hx, hg);
+    const Channels ch(a, s, b, p);
+    f32x8 m1 = {}, m2 = {};
+    each_group(p, s, p.c, [&](int j, int g) {
+        const float2 t = joined[int64_t(b) * a.groups + g];
+        m1[j] = t.x;
+        m2[j] = t.y;
+    });
+    apply_backward<T, kFull, kSilu>(a, p, ch, hx, hg, m1, m2);
 }
 
 constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -485,26 +642,26 @@ Pieces pieces_of(const Shape &s, int32_t n_struct, int32_t channels, int32_t gro
     return w;
 }
 
-template <class T, bool kSilu>
+template <class T, bool kFull, bool kSilu>
 hipError_t forward(const GroupNormArgs &a, hipStream_t stream) {
     const Shape s = shape_of(a.rows, a.n_struct, a.channels, a.groups);
     const dim3 grid(static_cast<unsigned>(int64_t(a.n_struct) * s.splits * s.n_slabs)), threads(kThreads);
     if (s.splits == 1) {
-        k_forward<T, kSilu><<<grid, threads, 0, stream>>>(a, s);
+        k_forward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s);
         return hipGetLastError();
     }
     double2 *partial = static_cast<double2 *>(a.workspace);
-    k_statistics<T><<<grid, threads, 0, stream>>>(a, s, partial);
+    k_statistics<T, kFull><<<grid, threads, 0, stream>>>(a, s, partial);
     const dim3 join(static_cast<unsigned>((int64_t(a.n_struct) * a.groups + 3) / 4));
     k_join_statistics<<<join, threads, 0, stream>>>(a, s, partial);
-    k_apply<T, kSilu><<<grid, threads, 0, stream>>>(a, s);
+    k_apply<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s);
     return hipGetLastError();
 }
 
-template <class T, bool kSilu>
+template <class T, bool kFull, bool kSilu>
 hipError_t backward(const GroupNormArgs &a, hipStream_t stream) {
     const bool params = a.grad_weight || a.grad_bias;
-    const int channel_blocks = params ? (a.channels + 15) / 16 : 0;
+    const int channel_blocks = params ? (a.channels + kJoinChannels - 1) / kJoinChannels : 0;
     const dim3 threads(kThreads);
     if (a.rows == 0 || a.n_struct == 0) {  // no parts: zeros
         if (params)
@@ -519,22 +676,30 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t stream) {
     float *column = params ? reinterpret_cast<float *>(ws + w.column) : nullptr;
     const dim3 grid(static_cast<unsigned>(int64_t(a.n_struct) * s.splits * s.n_slabs));
     if (s.splits == 1) {
-        k_backward<T, kSilu><<<grid, threads, 0, stream>>>(a, s, column);
+        k_backward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, column);
         if (params) k_join_gradients<<<dim3(channel_blocks), threads, 0, stream>>>(a, s, partial, joined, column, 0);
         return hipGetLastError();
     }
-    k_gradient_sums<T, kSilu><<<grid, threads, 0, stream>>>(a, s, column, partial);
+    k_gradient_sums<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, column, partial);
     const int join_blocks = a.grad_x ? static_cast<int>((int64_t(a.n_struct) * a.groups + 3) / 4) : 0;
     k_join_gradients<<<dim3(join_blocks + channel_blocks), threads, 0, stream>>>(a, s, partial, joined, column,
                                                                                 join_blocks);
-    if (a.grad_x) k_apply_backward<T, kSilu><<<grid, threads, 0, stream>>>(a, s, joined);
+    if (a.grad_x) k_apply_backward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, joined);
     return hipGetLastError();
+}
+
+template <class T, bool kFull>
+hipError_t run(const GroupNormArgs &a, bool back, hipStream_t stream) {
+    if (back) return a.silu ? backward<T, kFull, true>(a, stream) : backward<T, kFull, false>(a, stream);
+    return a.silu ? forward<T, kFull, true>(a, stream) : forward<T, kFull, false>(a, stream);
 }
 
 template <class T>
 hipError_t run(const GroupNormArgs &a, bool back, hipStream_t stream) {
-    if (back) return a.silu ? backward<T, true>(a, stream) : backward<T, false>(a, stream);
-    return a.silu ? forward<T, true>(a, stream) : forward<T, false>(a, stream);
+    // whether every slab's channels come in whole pieces of eight
+    const int gps = a.n_struct && a.rows ? shape_of(a.rows, a.n_struct, a.channels, a.groups).gps : 1;
+    const bool full = a.channels % 8 == 0 && gps * (a.channels / a.groups) % 8 == 0;
+    return full ? run<T, true>(a, back, stream) : run<T, false>(a, back, stream);
 }
 
 hipError_t run(oeq_dtype dtype, const GroupNormArgs &a, bool back, hipStream_t stream) {

@@ -164,8 +164,10 @@ def oeq_group_norm_bwd(x, ptr, n_groups: int, mean, rstd, grad_out, weight=None,
             gx = x.new_empty((rows, C))
         else:
             gx, ld_gx = out, _like(out, x, dev, "grad_x")
-    gw = torch.empty((C,), dtype=_F32, device=x.device) if "weight" in need else None
-    gb = torch.empty((C,), dtype=_F32, device=x.device) if "bias" in need else None
+    gw = gb = None
+    if "weight" in need or "bias" in need:
+        both = torch.empty((2, C), dtype=_F32, device=x.device).unbind(0)
+        gw, gb = (t if n in need else None for t, n in zip(both, ("weight", "bias")))
     keep, ws, nbytes = _scratch(nbytes, workspace, x.device)
     st = lib().oeq_group_norm_bwd(code, rows, B, C, n_groups, _act(act), ptr.data_ptr(), x.data_ptr(), ld, w, b, mu,
                                   rs, grad_out.data_ptr(), ld_g, None if gx is None else gx.data_ptr(), ld_gx,
