@@ -82,40 +82,99 @@ __device__ __forceinline__ f32x8 column_operand<float>(const float *tile, int ti
     return v;
 }
 
+// Keeps a branch that is seldom taken a branch: its work is not done ahead and selected.
+__device__ __forceinline__ void rare() { asm volatile(""); }
+
 // Rows of a strided operand on their way to LDS: kRows x kDim elements by kThreads threads,
-// in pieces of eight.  `fetch` reads rows first .. first + kRows - 1, rows past `last` in place
-// of which row `last` is read (its values are not used); `store` writes them, with zeros for
-// rows whose bit is not set and for columns past the head's dimension.
+// in pieces of eight, kLanes threads a row.  `fetch` reads the rows, `store` writes them with
+// zeros for rows whose bit in `valid` is not set and for columns past the head's dimension.
 template <class T, int kRows, int kDim, int kThreads>
 struct RowStage {
-    static constexpr int kPerRow = kDim / 8, kTotal = kRows * kPerRow, kPieces = (kTotal + kThreads - 1) / kThreads;
+    static constexpr int kLanes = kDim <= 32 ? 4 : kDim <= 64 ? 8 : 16;
+    static constexpr int kStep = kThreads / kLanes;  // rows from one of a thread's pieces to the next
+    static constexpr int kPieces = (kRows + kStep - 1) / kStep;
+    static_assert(kRows % kStep == 0 || kPieces == 1, "every piece but a lone one is whole");
     vec8<T> v[kPieces];
+    int row, d;
+    bool reads;  // whether this thread's columns are in the head
 
-    template <class RowAddress>
-    __device__ __forceinline__ void fetch(int thread, int dim, RowAddress &&address) {
+    __device__ __forceinline__ RowStage(int thread, int dim)
+        : row(thread / kLanes), d(thread % kLanes * 8), reads(d < dim && row < kRows) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int piece = thread + i * kThreads, row = piece / kPerRow, d = piece % kPerRow * 8;
-            if (piece < kTotal && d < dim) v[i] = *reinterpret_cast<const vec8<T> *>(address(row) + d);
-        }
+        for (int i = 0; i < kPieces; ++i) v[i] = vec8<T>(T(0.f));  // columns past the head stay zero
     }
-    __device__ __forceinline__ void store(T *tile, int thread, int dim, uint64_t valid) const {
+
+    // The tile's rows, at base + row * stride.  Where they end within the tile, row `last` is read
+    // in place of those past it (and dropped by store).  One set of loads serves both: a value
+    // that came by two ways would be waited for here, to be copied, and not where it is used.
+    __device__ __forceinline__ void fetch(const T *base, int64_t stride, int last) {
+        if (!reads) return;
+        const T *at = base + row * stride + d;
+        int64_t off[kPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int piece = thread + i * kThreads, row = piece / kPerRow, d = piece % kPerRow * 8;
-            if (piece >= kTotal) continue;  // decided at compile time where the pieces divide evenly
-            vec8<T> o = v[i];
-            if (d >= dim || !(valid >> row & 1)) o = vec8<T>(T(0.f));
-            T *at = tile + row * kTileRow<T, kDim> + d;
+        for (int i = 0; i < kPieces; ++i) off[i] = i * (kStep * stride);
+        if (last < kRows - 1) {
+            rare();
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) off[i] = int64_t(min(row + i * kStep, last) - row) * stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) v[i] = *reinterpret_cast<const vec8<T> *>(at + off[i]);
+    }
+    __device__ __forceinline__ void store(T *tile, bool whole, uint64_t valid) {
+        if (d >= kDim || row >= kRows) return;
+        if (!whole) {
+            rare();
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if (!(valid >> (row + i * kStep) & 1)) v[i] = vec8<T>(T(0.f));
+            }
+        }
+        T *at = tile + row * kTileRow<T, kDim> + d;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i, at += kStep * kTileRow<T, kDim>) {
             if constexpr (sizeof(T) == 4) {
-                reinterpret_cast<f32x4 *>(at)[0] = __builtin_shufflevector(o, o, 0, 1, 2, 3);
-                reinterpret_cast<f32x4 *>(at)[1] = __builtin_shufflevector(o, o, 4, 5, 6, 7);
+                reinterpret_cast<f32x4 *>(at)[0] = __builtin_shufflevector(v[i], v[i], 0, 1, 2, 3);
+                reinterpret_cast<f32x4 *>(at)[1] = __builtin_shufflevector(v[i], v[i], 4, 5, 6, 7);
             } else {
-                *reinterpret_cast<vec8<T> *>(at) = o;
+                *reinterpret_cast<vec8<T> *>(at) = v[i];
             }
         }
     }
 };
+
+// K and V tiles of one structure and key head on their way to LDS, with the mask of the keys
+// that are there and visible.
+template <class T, int kKeys, int kDim, int kThreads>
+struct KeyStage {
+    RowStage<T, kKeys, kDim, kThreads> k, v;
+    int there = 0;         // keys of the tile that are there
+    uint32_t visible = 1;  // what the mask holds for this lane's key
+    __device__ __forceinline__ KeyStage(int thread, int dim) : k(thread, dim), v(thread, dim) {}
+    __device__ __forceinline__ void fetch(const AttnArgs &a, const T *k_base, const T *v_base, const uint8_t *mask, int keys,
+                                          int t) {
+        const int k0 = t * kKeys;
+        there = keys - k0;
+        if (mask) visible = mask[k0 + min(int(threadIdx.x & (kKeys - 1)), there - 1)];
+        k.fetch(k_base + int64_t(k0) * a.k_row, a.k_row, there - 1);
+        v.fetch(v_base + int64_t(k0) * a.v_row, a.v_row, there - 1);
+    }
+    // Writes both tiles and returns which keys are to be used (bit = key of the tile).
+    __device__ __forceinline__ uint64_t store(T *k_tile, T *v_tile) {
+        const uint64_t valid = __ballot(int(threadIdx.x & (kKeys - 1)) < there && visible);
+        k.store(k_tile, valid == ~0ull, valid);
+        v.store(v_tile, valid == ~0ull, valid);
+        return valid;
+    }
+};
+
+// f(i, used) for a lane's sixteen scores of the 32 keys whose bits are `valid`.
+template <class F>
+__device__ __forceinline__ void each_score(uint32_t valid, int half, F &&f) {
+    const uint32_t mine = valid >> (8 * half);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f(i, (mine & (1u << (16 * (i >> 3) + (i & 7)))) != 0);
+}
 
 // Orders a wave's own LDS writes before its reads (LDS serves a wave in order; this keeps the
 // compiler from moving them).
@@ -125,8 +184,15 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Value of the lane 32 away.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+// Maximum and sum over the two halves' lanes of a column.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // Which structure, key head and rows a workgroup has.  Query rows of one key head are
 // numbered r = query * share + head within the share, so heads that share keys share the tile.
@@ -139,9 +205,8 @@ struct Place {
 };
 
 template <int kTile>
-__device__ __forceinline__ Place place_of(const AttnArgs &a, bool by_query, int splits, int64_t slots) {
+__device__ __forceinline__ Place place_of(const AttnArgs &a, int64_t item, bool by_query, int splits, int64_t slots) {
     Place p;
-    int64_t item = blockIdx.x;
     p.split = static_cast<int>(item % splits);
     item /= splits;
     const int64_t slot = item % slots;

@@ -158,7 +158,7 @@ oeq_status attn_args(const oeq_attn_desc *d, ro::AttnArgs *a) {
         if (stride < 0 || stride * es % 16)
             return fail(OEQ_ERR_INVALID_ARG, "strides must be non-negative multiples of 16 bytes");
     constexpr int64_t grid = int64_t(1) << 24;  // a launch holds fewer than 2^32 threads
-    if (d->n_struct && (ro::cross_attn_fwd_blocks(*a) >= grid || ro::cross_attn_bwd_blocks(*a) >= grid))
+    if (d->n_struct && (ro::cross_attn_fwd_blocks(d->dtype, *a) >= grid || ro::cross_attn_bwd_blocks(d->dtype, *a) >= grid))
         return fail(OEQ_ERR_UNSUPPORTED, "too many rows and heads for one launch");
     return OEQ_OK;
 }
@@ -268,8 +268,8 @@ oeq_status oeq_cross_attn_workspace_size(const oeq_attn_desc *desc, size_t *fwd_
     return guarded([&]() -> oeq_status {
         ro::AttnArgs a;
         OEQ_TRY(attn_args(desc, &a));
-        if (fwd_bytes) *fwd_bytes = a.n_struct && a.q_rows ? ro::cross_attn_fwd_workspace(a) : 0;
-        if (bwd_bytes) *bwd_bytes = a.n_struct ? ro::cross_attn_bwd_workspace(a) : 0;
+        if (fwd_bytes) *fwd_bytes = a.n_struct && a.q_rows ? ro::cross_attn_fwd_workspace(desc->dtype, a) : 0;
+        if (bwd_bytes) *bwd_bytes = a.n_struct ? ro::cross_attn_bwd_workspace(desc->dtype, a) : 0;
         return OEQ_OK;
     });
 }
@@ -285,7 +285,7 @@ oeq_status oeq_cross_attn_fwd(const oeq_attn_desc *desc, const int32_t *q_ptr, c
         if (!out || !lse) return fail(OEQ_ERR_INVALID_ARG, "out or lse is NULL");
         OEQ_TRY(check_aligned(out, 16, "out"));
         OEQ_TRY(check_aligned(lse, 4, "lse"));
-        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_fwd_workspace(a)));
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_fwd_workspace(desc->dtype, a)));
         a.out = out, a.lse = lse, a.workspace = workspace;
         return from_hip(ro::cross_attn_fwd(desc->dtype, a, static_cast<hipStream_t>(stream)), "cross attention");
     });
@@ -305,7 +305,7 @@ oeq_status oeq_cross_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, c
             OEQ_TRY(check_aligned(p, 16, "out, grad_out and the gradients"));
         OEQ_TRY(check_aligned(lse, 4, "lse"));
         if (a.n_struct == 0 || (!grad_q && !grad_k && !grad_v)) return OEQ_OK;
-        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_bwd_workspace(a)));
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::cross_attn_bwd_workspace(desc->dtype, a)));
         a.out = const_cast<void *>(out), a.lse = const_cast<float *>(lse), a.grad_out = grad_out;
         a.grad_q = grad_q, a.grad_k = grad_k, a.grad_v = grad_v, a.workspace = workspace;
         return from_hip(ro::cross_attn_bwd(desc->dtype, a, static_cast<hipStream_t>(stream)),

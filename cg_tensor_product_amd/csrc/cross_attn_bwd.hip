@@ -2,15 +2,19 @@
 // log sums, f the dropout factors (0 or 1 / share kept) and delta = sum_d grad_out out:
 //   grad_v = (p f)^T grad_out            dp = (grad_out v^T) f
 //   ds = p (dp - delta)                  grad_q = scale ds k,  grad_k = scale ds^T q
-// Three kernels and no atomics:
-//   k_delta        one pass over out and grad_out;
-//   k_grad_keys    a wave owns 32 keys (k, v and both gradients in registers) and walks the
-//                  query rows of the structure, all heads that share the keys among them, so
-//                  the sum over shared heads needs no further step;
-//   k_grad_queries a wave owns 32 query rows and walks the keys, like the forward.
-// Scores are formed twice (7 products of the minimal 5); the alternative, one kernel that adds
-// into grad_q, needs atomics or a partial grad_q for each tile of keys.  With few workgroups
-// the walk is split over workgroups, whose fp32 partial sums a last kernel adds in order.
+// One kernel in two roles, and no atomics:
+//   grad_keys     a wave owns 32 keys (k, v and both gradients in registers) and walks the
+//                 query rows of the structure, all heads that share the keys among them, so
+//                 the sum over shared heads needs no further step;
+//   grad_queries  a wave owns 32 query rows and walks the keys, like the forward.
+// Both form delta themselves (from rows that they read anyway, and out), so nothing has to
+// run before.  Scores are formed twice (7 products of the minimal 5); the alternative, one walk
+// that adds into grad_q, needs atomics or a partial grad_q for each tile of keys.  With few
+// workgroups the walks are split over workgroups, whose fp32 partial sums a second kernel adds
+// in order.
+//
+// The product that gives dp starts from -delta / (factor of what is kept) in its accumulators,
+// so that a score's gradient is one multiplication, and the factor is applied to the sums.
 #include "attn_device.hpp"
 
 namespace oeq {
@@ -20,56 +24,107 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kKeyTile = 128;  // keys of a k_grad_keys workgroup
+constexpr int kKeyTile = 128;  // keys of a workgroup that owns keys
 constexpr int kRowTile = 32;   // query rows of a step of its walk
 
 struct Bwd {
-    float *delta;      // [query row, head]
-    float *part_q;     // [split][query row, head][dim]; NULL: one split, written directly
+    float *part_q;           // [split][query row, head][dim]
     float *part_k, *part_v;  // [split][key, key head][dim]
+    int q_splits, k_splits;  // 1: gradients are written directly
+    int64_t q_slots, k_slots;
+    int64_t key_blocks;  // workgroups that own keys; the rest own query rows
 };
 
-// exp2 argument of a row that saw nothing: every probability is zero.
-__device__ __forceinline__ float log2_sum(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2E; }
-
 // p from a score; fp32 forms scale s - lse in one rounding, since the difference is small
-// against its parts.
+// against its parts.  `lse` is in powers of two for 16-bit types, and +infinity for a row that
+// saw nothing, whose probabilities are zero.
 template <class T>
-__device__ __forceinline__ float probability(float s, float scale, float c, float lse, float lse2) {
+__device__ __forceinline__ float probability(float s, float scale, float c, float lse) {
     if (sizeof(T) == 4) return __builtin_amdgcn_exp2f(fmaf(s, scale, -lse) * kLog2E);
-    return __builtin_amdgcn_exp2f(fmaf(s, c, -lse2));
+    return __builtin_amdgcn_exp2f(fmaf(s, c, -lse));
+}
+template <class T>
+__device__ __forceinline__ float kept_lse(float lse) {
+    return lse == -INFINITY ? INFINITY : sizeof(T) == 4 ? lse : lse * kLog2E;
 }
 
-// kDim / 8 (up to a power of two) lanes a row.
-template <class T, int kLanes>
-__global__ void __launch_bounds__(kThreads) k_delta(AttnArgs a, float *delta) {
-    const int64_t n = a.q_rows * a.heads, at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-    const int d = threadIdx.x % kLanes * 8;
+template <class T>
+__device__ __forceinline__ float dot(vec8<T> a, vec8<T> b) {
+    const f32x8 x = to_f32<T>(a), y = to_f32<T>(b);
     float v = 0.f;
-    if (at < n && d < a.dim) {
-        const f32x8 o = to_f32<T>(load8(static_cast<const T *>(a.out) + at * a.dim + d));
-        const f32x8 g = to_f32<T>(load8(static_cast<const T *>(a.grad_out) + at * a.dim + d));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v = fmaf(o[j], g[j], v);
-    }
-#pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) v += __shfl_xor(v, off);
-    if (at < n && threadIdx.x % kLanes == 0) delta[at] = v;
+    for (int j = 0; j < 8; ++j) v = fmaf(x[j], y[j], v);
+    return v;
 }
+
+// Four consecutive columns of a gradient, to the fp32 partial sums or the result.
+template <class T>
+__device__ __forceinline__ void put4(float *part, void *out, int64_t at, f32x4 v) {
+    using V4 = T __attribute__((ext_vector_type(4)));
+    if (part)
+        *reinterpret_cast<f32x4 *>(part + at) = v;
+    else
+        *reinterpret_cast<V4 *>(static_cast<T *>(out) + at) = __builtin_convertvector(v, V4);
+}
+
+template <class T, int kDim>
+struct KeyLds {
+    static constexpr int kRow = kTileRow<T, kDim>;
+    // two buffers, so that a step needs one barrier
+    T q[2][kRowTile * kRow], g[2][kRowTile * kRow];
+    float lse[2][kRowTile], delta[2][kRowTile];  // delta as the accumulators start from it
+    uint32_t kept[kWaves][kRowTile];             // bit = key of the wave
+};
 
 template <class T, int kDim, bool kDrop>
-__global__ void __launch_bounds__(kThreads) k_grad_keys(AttnArgs a, Bwd out, int splits, int64_t slots) {
-    constexpr int kRow = kTileRow<T, kDim>, kSteps = kDim / 16, kOut = kDim / 32;
-    __shared__ __attribute__((aligned(16))) T q_tile[kRowTile * kRow], g_tile[kRowTile * kRow];
-    __shared__ __attribute__((aligned(16))) float row_lse[kRowTile], row_delta[kRowTile];
-    __shared__ __attribute__((aligned(16))) uint32_t kept[kDrop ? kWaves : 1][kRowTile];
-    const Place w = place_of<kKeyTile>(a, false, splits, slots);
+__device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, KeyLds<T, kDim> &lds) {
+    constexpr int kRow = KeyLds<T, kDim>::kRow, kSteps = kDim / 16, kOut = kDim / 32;
+    const Place w = place_of<kKeyTile>(a, blockIdx.x, false, out.k_splits, out.k_slots);
     if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int key = w.first + wave * 32 + (lane & 31);
     const bool key_ok = key < w.keys;
     const int64_t k_row = w.k_begin + (key_ok ? key : 0);
     const bool seen = key_ok && (!a.key_mask || a.key_mask[k_row]);
+
+    using Stage = RowStage<T, kRowTile, kDim, kThreads>;
+    Stage q_in(threadIdx.x, a.dim), g_in(threadIdx.x, a.dim), o_in(threadIdx.x, a.dim);
+    float lse_in = 0.f;
+    const int n_tiles = (w.rows + kRowTile - 1) / kRowTile, per = (n_tiles + out.k_splits - 1) / out.k_splits;
+    const int t_end = min(n_tiles, (w.split + 1) * per);
+    const auto row_of = [&](int r, int64_t *q_row) {  // rows past the end: the last one
+        r = min(r, w.rows - 1);
+        const int in = r / a.share, head = w.kv_head * a.share + (r - in * a.share);
+        *q_row = w.q_begin + in;
+        return head;
+    };
+    const auto fetch = [&](int t) {
+        int64_t at[Stage::kPieces];
+#pragma unroll
+        for (int i = 0; i < Stage::kPieces; ++i) {
+            int64_t q_row;
+            const int head = row_of(t * kRowTile + q_in.row + i * Stage::kStep, &q_row);
+            at[i] = (q_row * a.heads + head) * a.dim + q_in.d;
+            if (q_in.reads)
+                q_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.q) + q_row * a.q_row +
+                                                               head * a.q_head + q_in.d);
+        }
+        if (q_in.reads) {
+#pragma unroll
+            for (int i = 0; i < Stage::kPieces; ++i) {
+                g_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.grad_out) + at[i]);
+                o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
+            }
+        }
+        if (threadIdx.x < kRowTile) {
+            int64_t q_row;
+            const int r = t * kRowTile + threadIdx.x, head = row_of(r, &q_row);
+            lse_in = a.lse[q_row * a.heads + head];
+        }
+    };
+    int t = w.split * per;
+    if (t < t_end) fetch(t);
+
     vec8<T> kf[kSteps], vf[kSteps];
     {
         const T *k = static_cast<const T *>(a.k) + k_row * a.k_row + w.kv_head * a.k_head;
@@ -84,63 +139,52 @@ __global__ void __launch_bounds__(kThreads) k_grad_keys(AttnArgs a, Bwd out, int
     }
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
-    const float c = a.scale * kLog2E;
+    const float c = a.scale * kLog2E, start = -1.f / a.keep_scale;
     f32x16 gk[kOut] = {}, gv[kOut] = {};
 
-    const int n_tiles = (w.rows + kRowTile - 1) / kRowTile, per = (n_tiles + splits - 1) / splits;
-    const int t_end = min(n_tiles, (w.split + 1) * per);
-    RowStage<T, kRowTile, kDim, kThreads> q_in, g_in;
-    float lse_in = 0.f, delta_in = 0.f;
-    auto side_row = [&](int r, int64_t *q_row, int *head) {
-        r = min(r, w.rows - 1);
-        *q_row = w.q_begin + r / a.share;
-        *head = w.kv_head * a.share + r % a.share;
-    };
-    auto fetch = [&](int t) {
-        int64_t q_row;
-        int head;
-        q_in.fetch(threadIdx.x, a.dim, [&](int row) {
-            side_row(t * kRowTile + row, &q_row, &head);
-            return static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
-        });
-        g_in.fetch(threadIdx.x, a.dim, [&](int row) {
-            side_row(t * kRowTile + row, &q_row, &head);
-            return static_cast<const T *>(a.grad_out) + (q_row * a.heads + head) * a.dim;
-        });
-        if (threadIdx.x < kRowTile) {
-            side_row(t * kRowTile + threadIdx.x, &q_row, &head);
-            const bool in = t * kRowTile + int(threadIdx.x) < w.rows;
-            lse_in = in ? a.lse[q_row * a.heads + head] : -INFINITY;  // rows past the end count as unseen
-            delta_in = in ? out.delta[q_row * a.heads + head] : 0.f;
-        }
-    };
-    int t = w.split * per;
-    if (t < t_end) fetch(t);
-    for (; t < t_end; ++t) {
-        const int r0 = t * kRowTile;
-        const int in_tile = min(kRowTile, w.rows - r0);
-        __syncthreads();  // the last tile has been read
+    for (int buffer = 0; t < t_end; ++t, buffer ^= 1) {
+        const int r0 = t * kRowTile, in_tile = min(kRowTile, w.rows - r0);
+        const bool whole = in_tile == kRowTile;
         const uint64_t valid = (1ull << in_tile) - 1;
-        q_in.store(q_tile, threadIdx.x, a.dim, valid);
-        g_in.store(g_tile, threadIdx.x, a.dim, valid);
-        if (threadIdx.x < kRowTile) {
-            row_lse[threadIdx.x] = lse_in == -INFINITY ? INFINITY : sizeof(T) == 4 ? lse_in : lse_in * kLog2E;
-            row_delta[threadIdx.x] = delta_in;
+        T *q_tile = lds.q[buffer], *g_tile = lds.g[buffer];
+#pragma unroll
+        for (int i = 0; i < Stage::kPieces; ++i) {
+            const int row = q_in.row + i * Stage::kStep;
+            float v = q_in.reads ? dot<T>(g_in.v[i], o_in.v[i]) : 0.f;
+#pragma unroll
+            for (int off = 1; off < Stage::kLanes; off <<= 1) v += __shfl_xor(v, off);
+            if (q_in.d == 0 && row < kRowTile) lds.delta[buffer][row] = row < in_tile ? v * start : 0.f;
         }
+        q_in.store(q_tile, whole, valid);
+        g_in.store(g_tile, whole, valid);
+        // rows past the end count as rows that saw nothing
+        if (threadIdx.x < kRowTile) lds.lse[buffer][threadIdx.x] = static_cast<int>(threadIdx.x) < in_tile ? kept_lse<T>(lse_in) : INFINITY;
         if (kDrop) {
-            // 32 rows x 4 generator blocks of this wave's keys, two a lane; the bits of a row make a word
+            // 32 rows x 4 generator blocks of this wave's keys, two a lane; a row's bits make a word
+            wave_sync();
             int64_t q_row;
-            int head;
-            side_row(r0 + (lane & 31), &q_row, &head);
+            const int head = row_of(r0 + (lane & 31), &q_row);
             const uint32_t row = static_cast<uint32_t>(q_row * a.heads + head);
             const uint32_t block = static_cast<uint32_t>(w.first + wave * 32) / 8 + 2 * half;
             const uint32_t bits = keep_bits(g, block, row, a.threshold) | keep_bits(g, block + 1, row, a.threshold) << 8;
-            reinterpret_cast<uint16_t *>(kept[wave])[(lane & 31) * 2 + half] = static_cast<uint16_t>(bits);
+            reinterpret_cast<uint16_t *>(lds.kept[wave])[(lane & 31) * 2 + half] = static_cast<uint16_t>(bits);
         }
         __syncthreads();
-        if (t + 1 < t_end) fetch(t + 1);
+        fetch(min(t + 1, t_end - 1));  // at the end, again the last
 
-        f32x16 s = {}, dp = {};
+        f32x16 s = {}, dp;
+        float lse[16], none[16];  // none: what dp - delta is where the probability was dropped
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 16 * (i >> 1) + 8 * half + 4 * (i & 1);  // rows of the tile
+            const f32x4 l = *reinterpret_cast<const f32x4 *>(lds.lse[buffer] + at);
+            const f32x4 d = *reinterpret_cast<const f32x4 *>(lds.delta[buffer] + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lse[4 * i + j] = l[j];
+                dp[4 * i + j] = none[4 * i + j] = d[j];
+            }
+        }
         const int row = permuted_row(lane & 31);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(q_tile, kRow, row, 16 * i, half), kf[i]);
@@ -150,20 +194,25 @@ __global__ void __launch_bounds__(kThreads) k_grad_keys(AttnArgs a, Bwd out, int
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x8 p8, s8;
+            uint32_t kept[8];
+            if (kDrop) {
+                const uint4 *from = reinterpret_cast<const uint4 *>(lds.kept[wave] + 16 * h + 8 * half);
+                const uint4 x = from[0], y = from[1];
+                kept[0] = x.x, kept[1] = x.y, kept[2] = x.z, kept[3] = x.w;
+                kept[4] = y.x, kept[5] = y.y, kept[6] = y.z, kept[7] = y.w;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int at = 16 * h + 8 * half + j;  // the row of the tile
-                const float l = row_lse[at];
-                float p = seen ? probability<T>(s[8 * h + j], a.scale, c, l, l) : 0.f;
-                float d = dp[8 * h + j];
-                float pk = p;
+                const int i = 8 * h + j;
+                const float p = probability<T>(s[i], a.scale, c, lse[i]);
                 if (kDrop) {
-                    const bool keep = kept[wave][at] >> (lane & 31) & 1;
-                    pk = keep ? p : 0.f;
-                    d = keep ? d * a.keep_scale : 0.f;
+                    const bool keep = kept[j] & (1u << (lane & 31));
+                    p8[j] = keep ? p : 0.f;
+                    s8[j] = p * (keep ? dp[i] : none[i]);
+                } else {
+                    p8[j] = p;
+                    s8[j] = p * dp[i];
                 }
-                p8[j] = pk;
-                s8[j] = p * (d - row_delta[at]);
             }
             pf[h] = from_f32<T>(p8);
             sf[h] = from_f32<T>(s8);
@@ -178,8 +227,9 @@ __global__ void __launch_bounds__(kThreads) k_grad_keys(AttnArgs a, Bwd out, int
         }
     }
     if (!key_ok) return;
-    const int64_t n = a.k_rows * a.kv_heads, at = k_row * a.kv_heads + w.kv_head;
-    using V4 = T __attribute__((ext_vector_type(4)));
+    const bool split = out.k_splits > 1;
+    const int64_t at = (split ? int64_t(w.split) * a.k_rows * a.kv_heads : 0) + k_row * a.kv_heads + w.kv_head;
+    const float k_factor = a.scale * a.keep_scale, v_factor = a.keep_scale;
 #pragma unroll
     for (int d = 0; d < kOut; ++d) {
 #pragma unroll
@@ -188,31 +238,24 @@ __global__ void __launch_bounds__(kThreads) k_grad_keys(AttnArgs a, Bwd out, int
             if (col < a.dim) {
                 f32x4 k = {gk[d][4 * i], gk[d][4 * i + 1], gk[d][4 * i + 2], gk[d][4 * i + 3]};
                 f32x4 v = {gv[d][4 * i], gv[d][4 * i + 1], gv[d][4 * i + 2], gv[d][4 * i + 3]};
-                // a key that is not seen has no gradient, whatever the rows hold
-                k = seen ? k * a.scale : f32x4{};
-                v = seen ? v * a.keep_scale : f32x4{};
-                if (splits > 1) {
-                    const int64_t to = (w.split * n + at) * a.dim + col;
-                    if (a.grad_k) *reinterpret_cast<f32x4 *>(out.part_k + to) = k;
-                    if (a.grad_v) *reinterpret_cast<f32x4 *>(out.part_v + to) = v;
-                } else {
-                    const int64_t to = at * a.dim + col;
-                    if (a.grad_k) *reinterpret_cast<V4 *>(static_cast<T *>(a.grad_k) + to) = __builtin_convertvector(k, V4);
-                    if (a.grad_v) *reinterpret_cast<V4 *>(static_cast<T *>(a.grad_v) + to) = __builtin_convertvector(v, V4);
-                }
+                // a key that is not seen has no gradient, whatever its scores were
+                k = seen ? k * k_factor : f32x4{};
+                v = seen ? v * v_factor : f32x4{};
+                if (a.grad_k) put4<T>(split ? out.part_k : nullptr, a.grad_k, at * a.dim + col, k);
+                if (a.grad_v) put4<T>(split ? out.part_v : nullptr, a.grad_v, at * a.dim + col, v);
             }
         }
     }
 }
 
 template <class T, int kDim, bool kSplitKeys>
-struct Tiles {
+struct QueryTiles {
     static constexpr int kKeys = 32;
     static constexpr int kRow = kTileRow<T, kDim>;
     static constexpr int kRows = kSplitKeys ? 32 : 128;  // query rows of a workgroup
     static constexpr int kStage = kSplitKeys ? 64 : kThreads;
     static constexpr int kTile = kKeys * kRow;
-    static constexpr int kLds = (kSplitKeys ? kWaves : 1) * 2 * kTile * int(sizeof(T));
+    static constexpr int kLds = (kSplitKeys ? kWaves : 2) * 2 * kTile * int(sizeof(T));
     static constexpr int kJoinRow = kDim + 4;
     static constexpr int kJoin = kSplitKeys ? kWaves * 32 * kJoinRow * 4 : 0;
     static constexpr int kBytes = kLds > kJoin ? kLds : kJoin;
@@ -221,69 +264,68 @@ struct Tiles {
 // The waves share tiles of keys, or with kSplitKeys (few query rows) take them in turn, as in
 // the forward.
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
-__global__ void __launch_bounds__(kThreads) k_grad_queries(AttnArgs a, Bwd out, int splits, int64_t slots) {
-    using C = Tiles<T, kDim, kSplitKeys>;
+__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, char *lds) {
+    using C = QueryTiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    __shared__ __attribute__((aligned(16))) char lds[C::kBytes];
-    const Place w = place_of<C::kRows>(a, true, splits, slots);
+    const Place w = place_of<C::kRows>(a, blockIdx.x - out.key_blocks, true, out.q_splits, out.q_slots);
     if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int thread = kSplitKeys ? lane : threadIdx.x;
     T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
+
+    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + out.q_splits - 1) / out.q_splits;
+    const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
+    const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
+    const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
+    const uint8_t *mask = a.key_mask ? a.key_mask + w.k_begin : nullptr;
+    KeyStage<T, kKeys, kDim, C::kStage> in(thread, a.dim);
+    int t = w.split * per + (kSplitKeys ? wave : 0);
+    if (t < t_end) in.fetch(a, k_base, v_base, mask, w.keys, t);
+
     const int r = w.first + (kSplitKeys ? 0 : wave * 32) + (lane & 31);
     const bool row_ok = r < w.rows;
     const int64_t q_row = w.q_begin + (row_ok ? r / a.share : 0);
     const int head = w.kv_head * a.share + (row_ok ? r % a.share : 0);
     const int64_t at = q_row * a.heads + head;
     vec8<T> qf[kSteps], gf[kSteps];
+    float delta = 0.f;
     {
         const T *q = static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
-        const T *g = static_cast<const T *>(a.grad_out) + at * a.dim;
+        const T *g = static_cast<const T *>(a.grad_out) + at * a.dim, *o = static_cast<const T *>(a.out) + at * a.dim;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int d = 16 * s + 8 * half;
-            const bool in = row_ok && d < a.dim;
-            qf[s] = in ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
-            gf[s] = in ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
+            const bool use = row_ok && d < a.dim;
+            qf[s] = use ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
+            gf[s] = use ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
+            if (use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
         }
     }
-    const float lse = row_ok ? a.lse[at] : -INFINITY, lse1 = lse == -INFINITY ? INFINITY : lse, lse2 = log2_sum(lse);
-    const float delta = row_ok ? out.delta[at] : 0.f;
+    const float none = sum_halves(delta) * (-1.f / a.keep_scale);
+    const float lse = kept_lse<T>(row_ok ? a.lse[at] : -INFINITY);
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
     const float c = a.scale * kLog2E;
     f32x16 gq[kOut] = {};
 
-    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
-    const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
-    const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
-    const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
-    const uint8_t *mask = a.key_mask ? a.key_mask + w.k_begin : nullptr;
-    RowStage<T, kKeys, kDim, C::kStage> k_in, v_in;
-    uint32_t visible = 0;
-    auto fetch = [&](int t) {
-        const int k0 = t * kKeys, last = w.keys - 1;
-        const int key = k0 + (lane & 31);
-        visible = key <= last && (!mask || mask[key]);
-        k_in.fetch(thread, a.dim, [&](int row) { return k_base + int64_t(min(k0 + row, last)) * a.k_row; });
-        v_in.fetch(thread, a.dim, [&](int row) { return v_base + int64_t(min(k0 + row, last)) * a.v_row; });
-    };
-    int t = w.split * per + (kSplitKeys ? wave : 0);
-    if (t < t_end) fetch(t);
-    for (; t < t_end; t += t_step) {
-        const uint64_t valid = __ballot(visible);
-        if (kSplitKeys) wave_sync(); else __syncthreads();
-        k_in.store(k_tile, thread, a.dim, valid);
-        v_in.store(v_tile, thread, a.dim, valid);
+    for (int buffer = 0; t < t_end; t += t_step) {
+        if (kSplitKeys) wave_sync();
+        const uint64_t valid = in.store(k_tile, v_tile);
         if (kSplitKeys) wave_sync(); else __syncthreads();
         const int k0 = t * kKeys;
-        if (t + t_step < t_end) fetch(t + t_step);
-        f32x16 s = {}, dp = {};
+        in.fetch(a, k_base, v_base, mask, w.keys, min(t + t_step, t_end - 1));
+        f32x16 s = {}, dp;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] = none;
         const int row = permuted_row(lane & 31);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(v_tile, kRow, row, 16 * i, half), gf[i]);
+        if (valid != ~0ull) {
+            rare();
+            each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
+        }
         vec8<T> sf[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -291,11 +333,8 @@ __global__ void __launch_bounds__(kThreads) k_grad_queries(AttnArgs a, Bwd out, 
             const uint32_t keep = kDrop ? keep_bits(g, (k0 + 16 * h) / 8 + half, static_cast<uint32_t>(at), a.threshold) : 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int key = 16 * h + 8 * half + j;
-                const float p = valid >> key & 1 ? probability<T>(s[8 * h + j], a.scale, c, lse1, lse2) : 0.f;
-                float d = dp[8 * h + j];
-                if (kDrop) d = (keep >> j & 1) ? d * a.keep_scale : 0.f;
-                s8[j] = p * (d - delta);
+                const float p = probability<T>(s[8 * h + j], a.scale, c, lse);
+                s8[j] = p * (!kDrop || (keep & (1u << j)) ? dp[8 * h + j] : none);
             }
             sf[h] = from_f32<T>(s8);
         }
@@ -304,25 +343,23 @@ __global__ void __launch_bounds__(kThreads) k_grad_queries(AttnArgs a, Bwd out, 
 #pragma unroll
             for (int h = 0; h < 2; ++h) gq[d] = mma(gq[d], column_operand(k_tile, kRow, 16 * h, 32 * d, lane), sf[h]);
         }
+        if (!kSplitKeys) {
+            k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
+            v_tile = k_tile + C::kTile;
+        }
     }
-    const int64_t n = a.q_rows * a.heads;
+    const bool split = out.q_splits > 1;
+    const int64_t part = split ? int64_t(w.split) * a.q_rows * a.heads : 0;
+    const float factor = a.scale * a.keep_scale;
     if (!kSplitKeys) {
         if (!row_ok) return;
-        using V4 = T __attribute__((ext_vector_type(4)));
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int col = 32 * d + 8 * i + 4 * half;
-                if (col < a.dim) {
-                    f32x4 v = {gq[d][4 * i], gq[d][4 * i + 1], gq[d][4 * i + 2], gq[d][4 * i + 3]};
-                    v *= a.scale;
-                    if (splits > 1)
-                        *reinterpret_cast<f32x4 *>(out.part_q + (w.split * n + at) * a.dim + col) = v;
-                    else
-                        *reinterpret_cast<V4 *>(static_cast<T *>(a.grad_q) + at * a.dim + col) =
-                            __builtin_convertvector(v, V4);
-                }
+                const f32x4 v = {gq[d][4 * i], gq[d][4 * i + 1], gq[d][4 * i + 2], gq[d][4 * i + 3]};
+                if (col < a.dim) put4<T>(split ? out.part_q : nullptr, a.grad_q, (part + at) * a.dim + col, v * factor);
             }
         }
         return;
@@ -338,9 +375,9 @@ __global__ void __launch_bounds__(kThreads) k_grad_queries(AttnArgs a, Bwd out, 
         }
     }
     __syncthreads();
-    const int jr = threadIdx.x >> 3, row = w.first + jr;  // eight threads a row
-    if (row >= w.rows) return;
-    const int64_t to = (w.q_begin + row / a.share) * a.heads + w.kv_head * a.share + row % a.share;
+    const int jr = threadIdx.x >> 3, jrow = w.first + jr;  // eight threads a row
+    if (jrow >= w.rows) return;
+    const int64_t to = (w.q_begin + jrow / a.share) * a.heads + w.kv_head * a.share + jrow % a.share;
     for (int col = (threadIdx.x & 7) * 8; col < a.dim; col += 64) {
         f32x8 v = {};
 #pragma unroll
@@ -349,22 +386,47 @@ __global__ void __launch_bounds__(kThreads) k_grad_queries(AttnArgs a, Bwd out, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += from[j];
         }
-        v *= a.scale;
-        if (splits > 1)
-            store8(out.part_q + (w.split * n + to) * a.dim + col, v);
+        v *= factor;
+        if (split)
+            store8(out.part_q + (part + to) * a.dim + col, v);
         else
             store8(static_cast<T *>(a.grad_q) + to * a.dim + col, from_f32<T>(v));
     }
 }
 
-// out = sum of `splits` fp32 arrays of n values (a multiple of eight), in order.
+// Two workgroups a compute unit, where that does not leave too few registers: against one, D = 96
+// takes 166 us for 279 and D = 128 239 for 328 (bf16, 4 structures of 1024 query rows and 2048
+// states, 8 heads over 4); fp32 at D = 128 would take 1369 for 1102.
+template <class T, int kDim, bool kDrop, bool kSplitKeys>
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 : 1) k_backward(AttnArgs a, Bwd out) {
+    constexpr int kKeyBytes = int(sizeof(KeyLds<T, kDim>)), kQueryBytes = QueryTiles<T, kDim, kSplitKeys>::kBytes;
+    __shared__ __attribute__((aligned(16))) char lds[kKeyBytes > kQueryBytes ? kKeyBytes : kQueryBytes];
+    if (blockIdx.x < out.key_blocks)
+        grad_keys<T, kDim, kDrop>(a, out, *reinterpret_cast<KeyLds<T, kDim> *>(lds));
+    else
+        grad_queries<T, kDim, kDrop, kSplitKeys>(a, out, lds);
+}
+
+// out = sum of `splits` fp32 arrays of n values (a multiple of eight), in order; up to three.
+struct Sum {
+    const float *part;
+    void *out;
+    int64_t n;
+    int splits;
+};
+struct Sums {
+    Sum job[3];
+};
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_add(const float *part, T *out, int64_t n, int splits) {
+__global__ void __launch_bounds__(kThreads) k_add(Sums sums) {
     const int64_t step = int64_t(gridDim.x) * kThreads * 8;
-    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < n; i += step) {
-        f32x8 v = load8(part + i);
-        for (int s = 1; s < splits; ++s) v += load8(part + s * n + i);
-        store8(out + i, from_f32<T>(v));
+    for (const Sum &j : sums.job) {
+        for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < j.n; i += step) {
+            f32x8 v = load8(j.part + i);
+#pragma unroll 8
+            for (int s = 1; s < j.splits; ++s) v += load8(j.part + s * j.n + i);
+            store8(static_cast<T *>(j.out) + i, from_f32<T>(v));
+        }
     }
 }
 
@@ -372,108 +434,99 @@ constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Choice {
     bool split_keys;
-    int q_splits, k_splits;  // of k_grad_queries (over keys), of k_grad_keys (over rows)
+    int q_splits, k_splits;
     int64_t q_slots, k_slots;
-    size_t delta, part_q, part_k, bytes;  // offsets of the workspace's pieces
-    size_t k_bytes;
+    size_t part_q, part_k, bytes;  // bytes of the partial sums; k for each of k and v
 };
 
-int splits_of(int64_t blocks, int64_t walk) {
-    int64_t s = (512 + blocks - 1) / blocks;  // two workgroups a compute unit
-    const int64_t most = walk / 256;          // 256 rows of the walk a split at least
-    s = s > most ? most : s;
+// Splits of a walk of `walk` rows, so that none is longer than `share`, what a workgroup has if the
+// work is spread evenly; 256 rows a split at least.
+int splits_of(int64_t walk, int64_t share) {
+    if (share < 256) share = 256;
+    const int64_t s = (walk + share / 2) / share;
     return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-Choice choose(const AttnArgs &a) {
+Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     Choice c{};
+    // Twice the workgroups the chip holds at once: walks half as long even out better than their
+    // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 107 us,
+    // 145 with walks of one round).
+    const int64_t fill = dtype != OEQ_F32 || a.dim <= 64 ? 1024 : 512;
     c.split_keys = a.q_rows * a.share <= 32 * int64_t(a.n_struct);
     c.q_slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
     c.k_slots = tile_slots(a.k_rows, a.n_struct, 1, kKeyTile);
-    c.q_splits = splits_of(c.q_slots * a.kv_heads, a.k_rows / a.n_struct);
-    c.k_splits = splits_of(c.k_slots * a.kv_heads, a.q_rows * a.share / a.n_struct);
-    c.part_q = up(static_cast<size_t>(a.q_rows) * a.heads * sizeof(float));
-    c.part_k = c.part_q + (c.q_splits > 1 ? up(static_cast<size_t>(c.q_splits) * a.q_rows * a.heads * a.dim * 4) : 0);
-    c.k_bytes = c.k_splits > 1 ? up(static_cast<size_t>(c.k_splits) * a.k_rows * a.kv_heads * a.dim * 4) : 0;
-    c.bytes = c.part_k + 2 * c.k_bytes;
+    const int64_t keys = a.k_rows / a.n_struct, rows = a.q_rows * a.share / a.n_struct;
+    const int64_t share = (c.q_slots * a.kv_heads * keys + c.k_slots * a.kv_heads * rows) / fill;
+    c.q_splits = splits_of(keys, share);
+    c.k_splits = splits_of(rows, share);
+    c.part_q = c.q_splits > 1 ? up(static_cast<size_t>(c.q_splits) * a.q_rows * a.heads * a.dim * 4) : 0;
+    c.part_k = c.k_splits > 1 ? up(static_cast<size_t>(c.k_splits) * a.k_rows * a.kv_heads * a.dim * 4) : 0;
+    c.bytes = c.part_q + 2 * c.part_k;
     return c;
 }
 
-unsigned grid_of(int64_t blocks) { return static_cast<unsigned>(blocks > (1 << 22) ? 1 << 22 : blocks); }
-
 template <class T, int kDim, bool kDrop>
-void launch(const AttnArgs &a, const Choice &c, const Bwd &out, hipStream_t stream) {
-    const dim3 threads(kThreads);
-    if (a.grad_k || a.grad_v) {
-        const dim3 grid(static_cast<unsigned>(c.k_slots * a.kv_heads * c.k_splits));
-        k_grad_keys<T, kDim, kDrop><<<grid, threads, 0, stream>>>(a, out, c.k_splits, c.k_slots);
-    }
-    if (a.grad_q && a.q_rows) {
-        const dim3 grid(static_cast<unsigned>(c.q_slots * a.kv_heads * c.q_splits));
-        if (c.split_keys)
-            k_grad_queries<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, out, c.q_splits, c.q_slots);
-        else
-            k_grad_queries<T, kDim, kDrop, false><<<grid, threads, 0, stream>>>(a, out, c.q_splits, c.q_slots);
-    }
+void launch(const AttnArgs &a, const Choice &c, const Bwd &out, int64_t blocks, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);
+    if (c.split_keys)
+        k_backward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, out);
+    else
+        k_backward<T, kDim, kDrop, false><<<grid, threads, 0, stream>>>(a, out);
 }
 
 template <class T, int kDim>
-void launch(const AttnArgs &a, const Choice &c, const Bwd &out, hipStream_t stream) {
-    if (a.q_rows) {
-        constexpr int kLanes = kDim <= 32 ? 4 : kDim <= 64 ? 8 : 16;
-        const int64_t n = a.q_rows * a.heads * kLanes;
-        k_delta<T, kLanes><<<dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream>>>(
-            a, out.delta);
-    }
+void launch(const AttnArgs &a, const Choice &c, const Bwd &out, int64_t blocks, hipStream_t stream) {
     if (a.threshold)
-        launch<T, kDim, true>(a, c, out, stream);
+        launch<T, kDim, true>(a, c, out, blocks, stream);
     else
-        launch<T, kDim, false>(a, c, out, stream);
+        launch<T, kDim, false>(a, c, out, blocks, stream);
 }
 
 template <class T>
-hipError_t backward(const AttnArgs &a, hipStream_t stream) {
-    const Choice c = choose(a);
+hipError_t backward(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
+    const Choice c = choose(dtype, a);
     char *ws = static_cast<char *>(a.workspace);
     Bwd out{};
-    out.delta = reinterpret_cast<float *>(ws);
-    out.part_q = reinterpret_cast<float *>(ws + c.part_q);
-    out.part_k = reinterpret_cast<float *>(ws + c.part_k);
-    out.part_v = reinterpret_cast<float *>(ws + c.part_k + c.k_bytes);
+    out.part_q = reinterpret_cast<float *>(ws);
+    out.part_k = reinterpret_cast<float *>(ws + c.part_q);
+    out.part_v = reinterpret_cast<float *>(ws + c.part_q + c.part_k);
+    out.q_splits = c.q_splits, out.k_splits = c.k_splits, out.q_slots = c.q_slots, out.k_slots = c.k_slots;
+    out.key_blocks = a.grad_k || a.grad_v ? c.k_slots * a.kv_heads * c.k_splits : 0;
+    const int64_t blocks = out.key_blocks + (a.grad_q ? c.q_slots * a.kv_heads * c.q_splits : 0);
     if (a.dim <= 32)
-        launch<T, 32>(a, c, out, stream);
+        launch<T, 32>(a, c, out, blocks, stream);
     else if (a.dim <= 64)
-        launch<T, 64>(a, c, out, stream);
+        launch<T, 64>(a, c, out, blocks, stream);
     else if (a.dim <= 96)
-        launch<T, 96>(a, c, out, stream);
+        launch<T, 96>(a, c, out, blocks, stream);
     else
-        launch<T, 128>(a, c, out, stream);
-    const auto add = [&](const float *part, void *to, int64_t n, int splits) {
-        if (to && splits > 1 && n)
-            k_add<T><<<dim3(grid_of((n / 8 + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream>>>(
-                part, static_cast<T *>(to), n, splits);
-    };
-    add(out.part_q, a.grad_q, a.q_rows * a.heads * a.dim, c.q_splits);
-    add(out.part_k, a.grad_k, a.k_rows * a.kv_heads * a.dim, c.k_splits);
-    add(out.part_v, a.grad_v, a.k_rows * a.kv_heads * a.dim, c.k_splits);
+        launch<T, 128>(a, c, out, blocks, stream);
+    const int64_t nq = a.grad_q && c.q_splits > 1 ? a.q_rows * a.heads * a.dim : 0;
+    const int64_t nk = c.k_splits > 1 ? a.k_rows * a.kv_heads * a.dim : 0;
+    const Sums sums = {{{out.part_q, a.grad_q, nq, c.q_splits},
+                        {out.part_k, a.grad_k, a.grad_k ? nk : 0, c.k_splits},
+                        {out.part_v, a.grad_v, a.grad_v ? nk : 0, c.k_splits}}};
+    const int64_t most = nq > nk ? nq : nk, grid = (most / 8 + kThreads - 1) / kThreads;
+    if (most)
+        k_add<T><<<dim3(static_cast<unsigned>(grid > 4096 ? 4096 : grid)), dim3(kThreads), 0, stream>>>(sums);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t cross_attn_bwd_workspace(const AttnArgs &a) { return choose(a).bytes; }
+size_t cross_attn_bwd_workspace(oeq_dtype dtype, const AttnArgs &a) { return choose(dtype, a).bytes; }
 
-int64_t cross_attn_bwd_blocks(const AttnArgs &a) {
-    const Choice c = choose(a);
-    const int64_t q = c.q_slots * a.kv_heads * c.q_splits, k = c.k_slots * a.kv_heads * c.k_splits;
-    return q > k ? q : k;
+int64_t cross_attn_bwd_blocks(oeq_dtype dtype, const AttnArgs &a) {
+    const Choice c = choose(dtype, a);
+    return c.q_slots * a.kv_heads * c.q_splits + c.k_slots * a.kv_heads * c.k_splits;
 }
 
 hipError_t cross_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
     switch (dtype) {
-        case OEQ_F32: return backward<float>(a, stream);
-        case OEQ_F16: return backward<f16>(a, stream);
-        case OEQ_BF16: return backward<bf16>(a, stream);
+        case OEQ_F32: return backward<float>(dtype, a, stream);
+        case OEQ_F16: return backward<f16>(dtype, a, stream);
+        case OEQ_BF16: return backward<bf16>(dtype, a, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -32,7 +32,7 @@ struct Tiles {
     static constexpr int kRows = kSplitKeys ? 32 : 128;  // query rows of a workgroup
     static constexpr int kStage = kSplitKeys ? 64 : kThreads;
     static constexpr int kTile = kKeys * kRow;  // elements of one K or V tile
-    static constexpr int kLds = (kSplitKeys ? kWaves : 1) * 2 * kTile * int(sizeof(T));
+    static constexpr int kLds = (kSplitKeys ? kWaves : 2) * 2 * kTile * int(sizeof(T));
     static constexpr int kJoinRow = kDim + 4;
     static constexpr int kJoin = kSplitKeys ? kWaves * 32 * (kJoinRow + 2) * 4 : 0;
     static constexpr int kBytes = kLds > kJoin ? kLds : kJoin;
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
     using C = Tiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32, kSub = kKeys / 32;
     __shared__ __attribute__((aligned(16))) char lds[C::kBytes];
-    const Place w = place_of<C::kRows>(a, true, splits, slots);
+    const Place w = place_of<C::kRows>(a, blockIdx.x, true, splits, slots);
     if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int thread = kSplitKeys ? lane : threadIdx.x;
@@ -83,26 +83,17 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
     const uint8_t *mask = a.key_mask ? a.key_mask + w.k_begin : nullptr;
 
-    RowStage<T, kKeys, kDim, C::kStage> k_in, v_in;
-    uint32_t visible = 0;
-    auto fetch = [&](int t) {
-        const int k0 = t * kKeys, last = w.keys - 1;
-        const int key = k0 + (lane & (kKeys - 1));
-        visible = key <= last && (!mask || mask[key]);
-        k_in.fetch(thread, a.dim, [&](int row) { return k_base + int64_t(min(k0 + row, last)) * a.k_row; });
-        v_in.fetch(thread, a.dim, [&](int row) { return v_base + int64_t(min(k0 + row, last)) * a.v_row; });
-    };
+    KeyStage<T, kKeys, kDim, C::kStage> in(thread, a.dim);
+    int buffer = 0;
 
     int t = w.split * per + (kSplitKeys ? wave : 0);
-    if (t < t_end) fetch(t);
+    if (t < t_end) in.fetch(a, k_base, v_base, mask, w.keys, t);
     for (; t < t_end; t += t_step) {
-        const uint64_t valid = __ballot(visible);
-        if (kSplitKeys) wave_sync(); else __syncthreads();  // the last tile has been read
-        k_in.store(k_tile, thread, a.dim, valid);
-        v_in.store(v_tile, thread, a.dim, valid);
+        if (kSplitKeys) wave_sync();
+        const uint64_t valid = in.store(k_tile, v_tile);
         if (kSplitKeys) wave_sync(); else __syncthreads();
         const int k0 = t * kKeys;
-        if (t + t_step < t_end) fetch(t + t_step);
+        in.fetch(a, k_base, v_base, mask, w.keys, min(t + t_step, t_end - 1));  // at the end, again the last
 
         f32x16 s[kSub];
 #pragma unroll
@@ -112,16 +103,12 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) s[u] = mma(s[u], row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
         }
-        const uint64_t all = kKeys == 64 ? ~0ull : 0xffffffffull;
-        if ((valid & all) != all) {
+        if (valid != ~0ull) {
+            rare();
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = 32 * u + 16 * (i >> 3) + 8 * half + (i & 7);
-                    if (!(valid >> key & 1)) s[u][i] = -INFINITY;
-                }
-            }
+            for (int u = 0; u < kSub; ++u)
+                each_score(static_cast<uint32_t>(valid >> (32 * u)), half,
+                           [&](int i, bool used) { s[u][i] = used ? s[u][i] : -INFINITY; });
         }
         float high = s[0][0];
 #pragma unroll
@@ -129,9 +116,10 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
 #pragma unroll
             for (int i = 0; i < 16; ++i) high = fmaxf(high, s[u][i]);
         }
-        high = fmaxf(high, other_half(high));
+        high = max_halves(high);
         // top = -inf (nothing seen yet) always moves on; a row that has seen nothing stays there
         if (__any((high - top) * c > kLag || (top == -INFINITY && high > -INFINITY))) {
+            rare();
             const float now = fmaxf(top, high);
             const float scale = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((top - now) * c);
             sum *= scale;
@@ -167,8 +155,13 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
                 o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u + 16, 32 * d, lane), p[1]);
             }
         }
+        // shared tiles have two buffers: one barrier a tile, since no wave is a whole tile ahead
+        if (!kSplitKeys) {
+            k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
+            v_tile = k_tile + C::kTile;
+        }
     }
-    sum += other_half(sum);
+    sum = sum_halves(sum);
 
     const int64_t at = q_row * a.heads + head;
     if (!kSplitKeys) {
@@ -265,33 +258,63 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
     }
 }
 
-// Joins the splits of one (query row, head) a wave.
-template <class T>
+// Joins the splits: eight columns of one (query row, head) a thread, kLanes threads for the
+// columns times kGroups that share the splits.
+template <class T, int kLanes, int kGroups>
 __global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Partial partial) {
-    const int64_t n = a.q_rows * a.heads, at = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-    if (at >= n) return;
-    const int lane = threadIdx.x & 63;
-    const float mine = lane < splits ? partial.lse[lane * n + at] : -INFINITY;  // at most 64 splits
-    float most = mine;
-    for (int off = 32; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
-    const float weight = mine == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine - most);
-    float total = weight;
-    for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off);
-    const bool seen = total > 0.f || total != total;
-    if (lane == 0) a.lse[at] = seen ? (most + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
-    const float norm = seen ? 1.f / total : 0.f;
-    T *out = static_cast<T *>(a.out) + at * a.dim;
-    for (int d = lane * 2; d < a.dim; d += 128) {
-        float u = 0.f, v = 0.f;
-        for (int i = 0; i < splits; ++i) {
-            const float *p = partial.out + (i * n + at) * a.dim + d;
-            const float w = __shfl(weight, i);
-            u += p[0] * w;
-            v += p[1] * w;
+    constexpr int kAhead = 4, kRow = kLanes * kGroups;
+    const int64_t n = a.q_rows * a.heads, at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kRow;
+    const int col = threadIdx.x % kLanes * 8, group = threadIdx.x % kRow / kLanes;
+    if (at >= n) return;  // whole rows of threads: the exchanges below stay within one
+    float most = -INFINITY, total = 0.f, bad = 0.f;
+    f32x8 v = {};
+    for (int first = group; first < splits; first += kGroups * kAhead) {
+        float l[kAhead];
+        f32x8 o[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int s = first + i * kGroups;
+            l[i] = s < splits ? partial.lse[s * n + at] : -INFINITY;
+            o[i] = s < splits && col < a.dim ? load8(partial.out + (s * n + at) * a.dim + col) : f32x8{};
         }
-        out[d] = T(u * norm);
-        out[d + 1] = T(v * norm);
+        float high = most;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            high = fmaxf(high, l[i]);
+            if (l[i] != l[i]) bad = l[i];  // the maximum leaves a NaN out
+        }
+        const float scale = most == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most - high);
+        v *= scale;
+        total *= scale;
+        most = high;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float weight = l[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(l[i] - most);
+            v += o[i] * weight;
+            total += weight;
+        }
     }
+    if (kGroups > 1) {
+        float high = most;
+#pragma unroll
+        for (int off = kLanes; off < kRow; off <<= 1) high = fmaxf(high, __shfl_xor(high, off));
+        const float scale = most == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most - high);
+        v *= scale;
+        total *= scale;
+        most = high;
+#pragma unroll
+        for (int off = kLanes; off < kRow; off <<= 1) {
+            total += __shfl_xor(total, off);
+            bad += __shfl_xor(bad, off);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += __shfl_xor(v[j], off);
+        }
+    }
+    total += bad;
+    if (group != 0 || col >= a.dim) return;
+    const bool seen = total > 0.f || total != total;
+    if (col == 0) a.lse[at] = seen ? (most + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+    store8(static_cast<T *>(a.out) + at * a.dim + col, from_f32<T>(v * (seen ? 1.f / total : 0.f)));
 }
 
 constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -307,8 +330,13 @@ Choice choose(const AttnArgs &a) {
     const int64_t rows = a.q_rows * a.share;
     c.split_keys = rows <= 32 * int64_t(a.n_struct);
     c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
+    // Splits until the workgroups fill the chip about once (256 compute units; four workgroups each
+    // at D <= 32, else two).  4 structures of 1024 query rows and 2048 states, 8 heads over 4:
+    // bf16, D = 64 takes 40 us with 512 workgroups, 49 with 768 and 45 with 1024; D = 32 takes
+    // 39, 37 and 34 us; fp32, D = 128 takes 305, 400 and 324 us.
+    const int64_t fill = 256 * (a.dim <= 32 ? 4 : 2);
     const int64_t base = c.slots * a.kv_heads, most = a.k_rows / a.n_struct / 256;  // 256 keys a split at least
-    int64_t splits = (512 + base - 1) / base;  // two workgroups a compute unit
+    int64_t splits = (fill + base / 2) / base;
     splits = splits > most ? most : splits;
     c.splits = static_cast<int>(splits < 1 ? 1 : splits > 64 ? 64 : splits);
     c.blocks = base * c.splits;
@@ -354,21 +382,35 @@ hipError_t forward(const AttnArgs &a, hipStream_t stream) {
         launch<T, 128>(a, c, partial, stream);
     if (c.splits > 1) {
         const int64_t n = a.q_rows * a.heads;
-        k_join<T><<<dim3(static_cast<unsigned>((n + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a, c.splits,
-                                                                                                       partial);
+        const auto join = [&](auto lanes) {
+            constexpr int kLanes = decltype(lanes)::value;
+            // many splits are shared by the threads of a wave, since they come with few rows
+            const int row = c.splits > 4 ? 64 : kLanes;
+            const dim3 grid(static_cast<unsigned>((n * row + kThreads - 1) / kThreads));
+            if (c.splits > 4)
+                k_join<T, kLanes, 64 / kLanes><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
+            else
+                k_join<T, kLanes, 1><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
+        };
+        if (a.dim <= 32)
+            join(std::integral_constant<int, 4>());
+        else if (a.dim <= 64)
+            join(std::integral_constant<int, 8>());
+        else
+            join(std::integral_constant<int, 16>());
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t cross_attn_fwd_workspace(const AttnArgs &a) {
+size_t cross_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) {
     const Choice c = choose(a);
     if (c.splits == 1) return 0;
     return partial_out(a, c) + up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * sizeof(float));
 }
 
-int64_t cross_attn_fwd_blocks(const AttnArgs &a) { return choose(a).blocks; }
+int64_t cross_attn_fwd_blocks(oeq_dtype, const AttnArgs &a) { return choose(a).blocks; }
 
 hipError_t cross_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
     switch (dtype) {

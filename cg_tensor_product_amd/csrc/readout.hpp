@@ -69,10 +69,10 @@ struct AttnArgs {
     void *workspace;
 };
 // Workspace bytes and the workgroups of the largest launch of each direction.
-size_t cross_attn_fwd_workspace(const AttnArgs &a);
-size_t cross_attn_bwd_workspace(const AttnArgs &a);
-int64_t cross_attn_fwd_blocks(const AttnArgs &a);
-int64_t cross_attn_bwd_blocks(const AttnArgs &a);
+size_t cross_attn_fwd_workspace(oeq_dtype dtype, const AttnArgs &a);
+size_t cross_attn_bwd_workspace(oeq_dtype dtype, const AttnArgs &a);
+int64_t cross_attn_fwd_blocks(oeq_dtype dtype, const AttnArgs &a);
+int64_t cross_attn_bwd_blocks(oeq_dtype dtype, const AttnArgs &a);
 hipError_t cross_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
 hipError_t cross_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
 
