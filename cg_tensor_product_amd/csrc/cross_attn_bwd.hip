@@ -7,8 +7,9 @@
 //                 query rows of the structure, all heads that share the keys among them, so
 //                 the sum over shared heads needs no further step;
 //   grad_queries  a wave owns 32 query rows and walks the keys, like the forward.
-// Both form delta themselves (from rows that they read anyway, and out), so nothing has to
-// run before.  Scores are formed twice (7 products of the minimal 5); the alternative, one walk
+// Both form delta themselves, from rows that they read anyway and from out.  Where out is
+// rounded to 16 bits and the structures have few states (kExactStates), that rounding would be
+// most of the gradients' error: there a pass of its own sums p dp in fp32 first.  Scores are formed twice (7 products of the minimal 5); the alternative, one walk
 // that adds into grad_q, needs atomics or a partial grad_q for each tile of keys.  With few
 // workgroups the walks are split over workgroups, whose fp32 partial sums a second kernel adds
 // in order.
@@ -26,8 +27,17 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kKeyTile = 128;  // keys of a workgroup that owns keys
 constexpr int kRowTile = 32;   // query rows of a step of its walk
+constexpr int kExactStates = 32;
+
+// The score gradients of 16-bit types go into their products as two terms, the rounded value and
+// the rest: rounded once, they and delta's rounding leave grad_q and grad_k with 1.4 to 1.9 times
+// the error that rounding the result alone does (10 to 4096 states), with the rest 1.0 to 1.2 from
+// 64 states on.  It costs 7 % of a decoder's training step (224 -> 239 us).
+template <class T>
+constexpr bool kRest = sizeof(T) == 2;
 
 struct Bwd {
+    float *delta;  // [query row, head]: -delta / factor of what is kept, or NULL: formed from out
     float *part_q;           // [split][query row, head][dim]
     float *part_k, *part_v;  // [split][key, key head][dim]
     int q_splits, k_splits;  // 1: gradients are written directly
@@ -67,6 +77,11 @@ __device__ __forceinline__ void put4(float *part, void *out, int64_t at, f32x4 v
         *reinterpret_cast<V4 *>(static_cast<T *>(out) + at) = __builtin_convertvector(v, V4);
 }
 
+__device__ __forceinline__ f32x8 load_lds8(const float *p) {
+    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 template <class T, int kDim>
 struct KeyLds {
     static constexpr int kRow = kTileRow<T, kDim>;
@@ -89,7 +104,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 
     using Stage = RowStage<T, kRowTile, kDim, kThreads>;
     Stage q_in(threadIdx.x, a.dim), g_in(threadIdx.x, a.dim), o_in(threadIdx.x, a.dim);
-    float lse_in = 0.f;
+    float lse_in = 0.f, delta_in = 0.f;
     const int n_tiles = (w.rows + kRowTile - 1) / kRowTile, per = (n_tiles + out.k_splits - 1) / out.k_splits;
     const int t_end = min(n_tiles, (w.split + 1) * per);
     const auto row_of = [&](int r, int64_t *q_row) {  // rows past the end: the last one
@@ -113,13 +128,14 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 #pragma unroll
             for (int i = 0; i < Stage::kPieces; ++i) {
                 g_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.grad_out) + at[i]);
-                o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
+                if (!out.delta) o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
             }
         }
         if (threadIdx.x < kRowTile) {
             int64_t q_row;
             const int r = t * kRowTile + threadIdx.x, head = row_of(r, &q_row);
             lse_in = a.lse[q_row * a.heads + head];
+            if (out.delta) delta_in = out.delta[q_row * a.heads + head];
         }
     };
     int t = w.split * per;
@@ -147,13 +163,18 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
         const bool whole = in_tile == kRowTile;
         const uint64_t valid = (1ull << in_tile) - 1;
         T *q_tile = lds.q[buffer], *g_tile = lds.g[buffer];
+        if (out.delta) {
+            if (threadIdx.x < kRowTile)
+                lds.delta[buffer][threadIdx.x] = static_cast<int>(threadIdx.x) < in_tile ? delta_in : 0.f;
+        } else {
 #pragma unroll
-        for (int i = 0; i < Stage::kPieces; ++i) {
-            const int row = q_in.row + i * Stage::kStep;
-            float v = q_in.reads ? dot<T>(g_in.v[i], o_in.v[i]) : 0.f;
+            for (int i = 0; i < Stage::kPieces; ++i) {
+                const int row = q_in.row + i * Stage::kStep;
+                float v = q_in.reads ? dot<T>(g_in.v[i], o_in.v[i]) : 0.f;
 #pragma unroll
-            for (int off = 1; off < Stage::kLanes; off <<= 1) v += __shfl_xor(v, off);
-            if (q_in.d == 0 && row < kRowTile) lds.delta[buffer][row] = row < in_tile ? v * start : 0.f;
+                for (int off = 1; off < Stage::kLanes; off <<= 1) v += __shfl_xor(v, off);
+                if (q_in.d == 0 && row < kRowTile) lds.delta[buffer][row] = row < in_tile ? v * start : 0.f;
+            }
         }
         q_in.store(q_tile, whole, valid);
         g_in.store(g_tile, whole, valid);
@@ -173,30 +194,30 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
         fetch(min(t + 1, t_end - 1));  // at the end, again the last
 
         f32x16 s = {}, dp;
-        float lse[16], none[16];  // none: what dp - delta is where the probability was dropped
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = 16 * (i >> 1) + 8 * half + 4 * (i & 1);  // rows of the tile
-            const f32x4 l = *reinterpret_cast<const f32x4 *>(lds.lse[buffer] + at);
-            const f32x4 d = *reinterpret_cast<const f32x4 *>(lds.delta[buffer] + at);
+            const f32x4 d = *reinterpret_cast<const f32x4 *>(lds.delta[buffer] + 16 * (i >> 1) + 8 * half + 4 * (i & 1));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lse[4 * i + j] = l[j];
-                dp[4 * i + j] = none[4 * i + j] = d[j];
-            }
+            for (int j = 0; j < 4; ++j) dp[4 * i + j] = d[j];
         }
         const int row = permuted_row(lane & 31);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(q_tile, kRow, row, 16 * i, half), kf[i]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(g_tile, kRow, row, 16 * i, half), vf[i]);
-        vec8<T> pf[2], sf[2];
+        vec8<T> pf[2], sf[2], sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f32x8 p8, s8;
+            // rows 16 h + 8 half + j of the tile; none: what dp - delta is where the probability was
+            // dropped.  Read again here rather than kept, where that saves spills (D = 96 with dropout
+            // 240 -> 212 us; at D = 128, which spills either way, 342 -> 378).
+            if (kDim < 128) asm volatile("" ::: "memory");
+            const int first = 16 * h + 8 * half;
+            f32x8 p8, s8, lse = load_lds8(lds.lse[buffer] + first), none;
             uint32_t kept[8];
             if (kDrop) {
-                const uint4 *from = reinterpret_cast<const uint4 *>(lds.kept[wave] + 16 * h + 8 * half);
+                none = load_lds8(lds.delta[buffer] + first);
+                const uint4 *from = reinterpret_cast<const uint4 *>(lds.kept[wave] + first);
                 const uint4 x = from[0], y = from[1];
                 kept[0] = x.x, kept[1] = x.y, kept[2] = x.z, kept[3] = x.w;
                 kept[4] = y.x, kept[5] = y.y, kept[6] = y.z, kept[7] = y.w;
@@ -204,11 +225,11 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int i = 8 * h + j;
-                const float p = probability<T>(s[i], a.scale, c, lse[i]);
+                const float p = probability<T>(s[i], a.scale, c, lse[j]);
                 if (kDrop) {
                     const bool keep = kept[j] & (1u << (lane & 31));
                     p8[j] = keep ? p : 0.f;
-                    s8[j] = p * (keep ? dp[i] : none[i]);
+                    s8[j] = p * (keep ? dp[i] : none[j]);
                 } else {
                     p8[j] = p;
                     s8[j] = p * dp[i];
@@ -216,13 +237,16 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
             }
             pf[h] = from_f32<T>(p8);
             sf[h] = from_f32<T>(s8);
+            if (kRest<T>) sl[h] = from_f32<T>(s8 - to_f32<T>(sf[h]));
         }
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 gv[d] = mma(gv[d], column_operand(g_tile, kRow, 16 * h, 32 * d, lane), pf[h]);
-                gk[d] = mma(gk[d], column_operand(q_tile, kRow, 16 * h, 32 * d, lane), sf[h]);
+                const vec8<T> q = column_operand(q_tile, kRow, 16 * h, 32 * d, lane);
+                gk[d] = mma(gk[d], q, sf[h]);
+                if (kRest<T>) gk[d] = mma(gk[d], q, sl[h]);
             }
         }
     }
@@ -262,18 +286,18 @@ struct QueryTiles {
 };
 
 // The waves share tiles of keys, or with kSplitKeys (few query rows) take them in turn, as in
-// the forward.
-template <class T, int kDim, bool kDrop, bool kSplitKeys>
-__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, char *lds) {
+// the forward.  kDelta: delta to out.delta in place of the gradient (one split).
+template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kDelta>
+__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, int64_t item, int splits, char *lds) {
     using C = QueryTiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const Place w = place_of<C::kRows>(a, blockIdx.x - out.key_blocks, true, out.q_splits, out.q_slots);
+    const Place w = place_of<C::kRows>(a, item, true, splits, out.q_slots);
     if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int thread = kSplitKeys ? lane : threadIdx.x;
     T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
 
-    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + out.q_splits - 1) / out.q_splits;
+    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
     const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
     const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
@@ -298,10 +322,11 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
             const bool use = row_ok && d < a.dim;
             qf[s] = use ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
             gf[s] = use ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
-            if (use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
+            if (!kDelta && !out.delta && use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
         }
     }
-    const float none = sum_halves(delta) * (-1.f / a.keep_scale);
+    const float none = kDelta ? 0.f : out.delta ? out.delta[at] : sum_halves(delta) * (-1.f / a.keep_scale);
+    float exact = 0.f;
     const float lse = kept_lse<T>(row_ok ? a.lse[at] : -INFINITY);
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
@@ -326,7 +351,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
             rare();
             each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
         }
-        vec8<T> sf[2];
+        vec8<T> sf[2], sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x8 s8;
@@ -335,20 +360,42 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
             for (int j = 0; j < 8; ++j) {
                 const float p = probability<T>(s[8 * h + j], a.scale, c, lse);
                 s8[j] = p * (!kDrop || (keep & (1u << j)) ? dp[8 * h + j] : none);
+                if (kDelta) exact -= s8[j];
             }
             sf[h] = from_f32<T>(s8);
+            if (kRest<T>) sl[h] = from_f32<T>(s8 - to_f32<T>(sf[h]));
         }
+        if constexpr (!kDelta) {
 #pragma unroll
-        for (int d = 0; d < kOut; ++d) {
+            for (int d = 0; d < kOut; ++d) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) gq[d] = mma(gq[d], column_operand(k_tile, kRow, 16 * h, 32 * d, lane), sf[h]);
+                for (int h = 0; h < 2; ++h) {
+                    const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
+                    gq[d] = mma(gq[d], k, sf[h]);
+                    if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
+                }
+            }
         }
         if (!kSplitKeys) {
             k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
             v_tile = k_tile + C::kTile;
         }
     }
-    const bool split = out.q_splits > 1;
+    if constexpr (kDelta) {
+        exact = sum_halves(exact);
+        if (!kSplitKeys) {
+            if (row_ok && half == 0) out.delta[at] = exact;
+            return;
+        }
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(lds);
+        if (half == 0) sums[wave * 32 + lane] = exact;
+        __syncthreads();
+        if (wave == 0 && half == 0 && row_ok)
+            out.delta[at] = sums[lane] + sums[32 + lane] + sums[64 + lane] + sums[96 + lane];
+        return;
+    }
+    const bool split = splits > 1;
     const int64_t part = split ? int64_t(w.split) * a.q_rows * a.heads : 0;
     const float factor = a.scale * a.keep_scale;
     if (!kSplitKeys) {
@@ -404,7 +451,13 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 :
     if (blockIdx.x < out.key_blocks)
         grad_keys<T, kDim, kDrop>(a, out, *reinterpret_cast<KeyLds<T, kDim> *>(lds));
     else
-        grad_queries<T, kDim, kDrop, kSplitKeys>(a, out, lds);
+        grad_queries<T, kDim, kDrop, kSplitKeys, false>(a, out, blockIdx.x - out.key_blocks, out.q_splits, lds);
+}
+
+template <class T, int kDim, bool kDrop, bool kSplitKeys>
+__global__ void __launch_bounds__(kThreads, 2) k_delta(AttnArgs a, Bwd out) {
+    __shared__ __attribute__((aligned(16))) char lds[QueryTiles<T, kDim, kSplitKeys>::kLds];
+    grad_queries<T, kDim, kDrop, kSplitKeys, true>(a, out, blockIdx.x, 1, lds);
 }
 
 // out = sum of `splits` fp32 arrays of n values (a multiple of eight), in order; up to three.
@@ -436,7 +489,7 @@ struct Choice {
     bool split_keys;
     int q_splits, k_splits;
     int64_t q_slots, k_slots;
-    size_t part_q, part_k, bytes;  // bytes of the partial sums; k for each of k and v
+    size_t delta, part_q, part_k, bytes;  // bytes of delta and of the partial sums; k for each of k and v
 };
 
 // Splits of a walk of `walk` rows, so that none is longer than `share`, what a workgroup has if the
@@ -452,7 +505,7 @@ Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     // Twice the workgroups the chip holds at once: walks half as long even out better than their
     // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 107 us,
     // 145 with walks of one round).
-    const int64_t fill = dtype != OEQ_F32 || a.dim <= 64 ? 1024 : 512;
+    const int64_t fill = 1024;
     c.split_keys = a.q_rows * a.share <= 32 * int64_t(a.n_struct);
     c.q_slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
     c.k_slots = tile_slots(a.k_rows, a.n_struct, 1, kKeyTile);
@@ -462,13 +515,21 @@ Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     c.k_splits = splits_of(rows, share);
     c.part_q = c.q_splits > 1 ? up(static_cast<size_t>(c.q_splits) * a.q_rows * a.heads * a.dim * 4) : 0;
     c.part_k = c.k_splits > 1 ? up(static_cast<size_t>(c.k_splits) * a.k_rows * a.kv_heads * a.dim * 4) : 0;
-    c.bytes = c.part_q + 2 * c.part_k;
+    c.delta = dtype != OEQ_F32 && keys <= kExactStates ? up(static_cast<size_t>(a.q_rows) * a.heads * sizeof(float)) : 0;
+    c.bytes = c.delta + c.part_q + 2 * c.part_k;
     return c;
 }
 
 template <class T, int kDim, bool kDrop>
 void launch(const AttnArgs &a, const Choice &c, const Bwd &out, int64_t blocks, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);
+    if constexpr (sizeof(T) == 2) {
+        const dim3 rows(static_cast<unsigned>(c.q_slots * a.kv_heads));
+        if (out.delta && c.split_keys)
+            k_delta<T, kDim, kDrop, true><<<rows, threads, 0, stream>>>(a, out);
+        else if (out.delta)
+            k_delta<T, kDim, kDrop, false><<<rows, threads, 0, stream>>>(a, out);
+    }
     if (c.split_keys)
         k_backward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, out);
     else
@@ -488,6 +549,8 @@ hipError_t backward(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
     const Choice c = choose(dtype, a);
     char *ws = static_cast<char *>(a.workspace);
     Bwd out{};
+    if (c.delta) out.delta = reinterpret_cast<float *>(ws);
+    ws += c.delta;
     out.part_q = reinterpret_cast<float *>(ws);
     out.part_k = reinterpret_cast<float *>(ws + c.part_q);
     out.part_v = reinterpret_cast<float *>(ws + c.part_q + c.part_k);
