@@ -38,9 +38,9 @@ def _head(t, name):
 
 
 def _typed(t, dtype, dev, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:  # -1 on the host
         raise TypeError(f"{name} must be a tensor on device cuda:{dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
@@ -48,7 +48,8 @@ def _dense(t, shape, dtype, dev, name):
     """Address of a contiguous operand (None: not given)."""
     if t is None:
         return None
-    _typed(t, dtype, dev, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
+        _typed(t, dtype, dev, name)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
@@ -97,7 +98,8 @@ def _scratch(nbytes, workspace, device):
 # ---------------------------------------------------------------------------
 
 def _structures(ptr, dev, name="ptr"):
-    _typed(ptr, _I32, dev, name)
+    if not isinstance(ptr, torch.Tensor) or ptr.get_device() != dev or ptr.dtype is not _I32:
+        _typed(ptr, _I32, dev, name)
     if ptr.dim() != 1 or ptr.shape[0] < 1 or not ptr.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of [structures + 1] values")
     return ptr.shape[0] - 1
@@ -228,7 +230,8 @@ def oeq_dropout_bwd(grad_out, p: float, rng, out=None):
 
 def _heads(t, shape, dtype, dev, name):
     """Row and head strides of a [rows, heads, dim] operand with contiguous heads."""
-    _typed(t, dtype, dev, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
+        _typed(t, dtype, dev, name)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     row, head, last = t.stride()
@@ -239,25 +242,27 @@ def _heads(t, shape, dtype, dev, name):
 
 
 @functools.lru_cache(maxsize=4096)
-def _attn_bytes(*fields):
+def _attn_desc(*fields):
+    """(descriptor, workspace bytes forward, backward), a function of sizes, strides and numbers."""
+    d = _AttnDesc(*fields)
     f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(_AttnDesc(*fields)), ctypes.byref(f), ctypes.byref(b)))
-    return f.value, b.value
+    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b)))
+    return ctypes.byref(d), f.value, b.value
 
 
 def oeq_cross_attn_workspace_size(q_shape, k_shape, n_struct: int, dtype=torch.float32):
     """Workspace bytes (forward, backward) for q of shape [Tq, H, D] and k, v of [Tk, Hkv, D]."""
     (tq, h, d), (tk, hk, _) = q_shape, k_shape
-    return _attn_bytes(_DTYPES[dtype], n_struct, h, hk, d, tq, tk, 0, 0, 0, 0, 0, 0, 1.0, 0.0)
+    return _attn_desc(_DTYPES[dtype], n_struct, h, hk, d, tq, tk, 0, 0, 0, 0, 0, 0, 1.0, 0.0)[1:]
 
 
 def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
-    """(device, descriptor fields, addresses of the operands both directions read)"""
+    """(device, what _attn_desc gives, addresses of the operands both directions read)"""
     code, dev = _head(q, "q")
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, dim]")
-    dt = q.dtype
-    tq, h, d = q.shape
+    dt, shape = q.dtype, q.shape
+    tq, h, d = shape
     tk, hk, _ = k.shape
     kv = (tk, hk, d)
     B = _structures(q_ptr, dev, "q_ptr")
@@ -265,11 +270,11 @@ def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
         raise ValueError("q_ptr and k_ptr must hold the same structures")
     mask = None
     if key_mask is not None:
-        mask = _dense(key_mask, (tk,), torch.bool if key_mask.dtype == torch.bool else _U8, dev, "key_mask")
-    fields = (code, B, h, hk, d, tq, tk, *_heads(q, q.shape, dt, dev, "q"), *_heads(k, kv, dt, dev, "k"),
-              *_heads(v, kv, dt, dev, "v"), d ** -0.5 if scale is None else scale, p_drop)
-    return dev, fields, (q_ptr.data_ptr(), k_ptr.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), mask,
-                         _dense(rng, (2,), _I64, dev, "rng"))
+        mask = _dense(key_mask, (tk,), torch.bool if key_mask.dtype is torch.bool else _U8, dev, "key_mask")
+    desc = _attn_desc(code, B, h, hk, d, tq, tk, *_heads(q, shape, dt, dev, "q"), *_heads(k, kv, dt, dev, "k"),
+                      *_heads(v, kv, dt, dev, "v"), d ** -0.5 if scale is None else scale, p_drop)
+    return dev, desc, (q_ptr.data_ptr(), k_ptr.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), mask,
+                       _dense(rng, (2,), _I64, dev, "rng"))
 
 
 def oeq_cross_attn_fwd(q, k, v, q_ptr, k_ptr, scale=None, key_mask=None, p_drop: float = 0.0, rng=None, out=None,
@@ -279,17 +284,17 @@ def oeq_cross_attn_fwd(q, k, v, q_ptr, k_ptr, scale=None, key_mask=None, p_drop:
     1 / sqrt(D); key_mask [Tk] (bool or uint8) is nonzero where a state is visible; rng (see
     oeq_dropout_fwd) is needed for p_drop > 0.  Rows and heads of q, k and v may be strided;
     out and lse (fp32 [Tq, H]) are contiguous."""
-    dev, fields, operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
+    dev, (desc, fwd_bytes, _), operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, q.shape, q.dtype, dev, "out")
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
     else:
         _dense(lse, q.shape[:2], _F32, dev, "lse")
-    keep, ws, nbytes = _scratch(_attn_bytes(*fields)[0], workspace, q.device)
-    st = lib().oeq_cross_attn_fwd(ctypes.byref(_AttnDesc(*fields)), *operands, out.data_ptr(), lse.data_ptr(), ws,
+    keep, ws, nbytes = _scratch(fwd_bytes, workspace, q.device)
+    st = lib().oeq_cross_attn_fwd(desc, *operands, out.data_ptr(), lse.data_ptr(), ws,
                                   nbytes, _raw_stream(dev))
     if st:
         _check(st)
@@ -300,15 +305,16 @@ def oeq_cross_attn_bwd(q, k, v, q_ptr, k_ptr, out, lse, grad_out, scale=None, ke
                        rng=None, need=("q", "k", "v"), grads=None, workspace=None):
     """(grad_q, grad_k, grad_v) of <grad_out, out> from the forward's operands, out and lse;
     entries not in `need` are None.  `grads` may supply preallocated gradients (contiguous)."""
-    dev, fields, operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
+    dev, (desc, _, bwd_bytes), operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng)
     saved = (_dense(out, q.shape, q.dtype, dev, "out"), _dense(lse, q.shape[:2], _F32, dev, "lse"),
              _dense(grad_out, q.shape, q.dtype, dev, "grad_out"))
     if grads is None:
-        grads = tuple(q.new_empty(t.shape) if n in need else None for n, t in (("q", q), ("k", k), ("v", k)))
+        grads = tuple(torch.empty_like(t, memory_format=torch.contiguous_format) if n in need else None
+                      for n, t in (("q", q), ("k", k), ("v", k)))
     addresses = tuple(_dense(g, t.shape, q.dtype, dev, n)
                       for g, t, n in zip(grads, (q, k, k), ("grad_q", "grad_k", "grad_v")))
-    keep, ws, nbytes = _scratch(_attn_bytes(*fields)[1], workspace, q.device)
-    st = lib().oeq_cross_attn_bwd(ctypes.byref(_AttnDesc(*fields)), *operands, *saved, *addresses, ws, nbytes,
+    keep, ws, nbytes = _scratch(bwd_bytes, workspace, q.device)
+    st = lib().oeq_cross_attn_bwd(desc, *operands, *saved, *addresses, ws, nbytes,
                                   _raw_stream(dev))
     if st:
         _check(st)
