@@ -205,22 +205,21 @@ struct Place {
 };
 
 template <int kTile>
-__device__ __forceinline__ Place place_of(const AttnArgs &a, int64_t item, bool by_query, int splits, int64_t slots) {
+__device__ __forceinline__ Place place_of(const AttnArgs &a, uint32_t item, bool by_query, int splits, int64_t n_slots) {
     Place p;
-    p.split = static_cast<int>(item % splits);
-    item /= splits;
-    const int64_t slot = item % slots;
-    p.kv_head = static_cast<int>(item / slots);
-    int64_t first;
-    const int32_t *ptr = by_query ? a.q_ptr : a.k_ptr;
-    const int per = by_query ? a.share : 1;
-    const int b = find_structure(ptr, a.n_struct, per, kTile, slot, &first);
-    const Span q = span_of(a.q_ptr, b, a.q_rows), k = span_of(a.k_ptr, b, a.k_rows);
+    const uint32_t slots = static_cast<uint32_t>(n_slots), rest = item / static_cast<uint32_t>(splits);
+    p.split = static_cast<int>(item - rest * splits);
+    p.kv_head = static_cast<int>(rest / slots);
+    const int64_t slot = rest - p.kv_head * slots;
+    const Owner at_slot = by_query ? find_structure(a.q_ptr, a.k_ptr, a.n_struct, a.share, kTile, slot)
+                                   : find_structure(a.k_ptr, a.q_ptr, a.n_struct, 1, kTile, slot);
+    const int32_t *qp = by_query ? at_slot.ptr : at_slot.other, *kp = by_query ? at_slot.other : at_slot.ptr;
+    const Span q = span_of(qp[0], qp[1], a.q_rows), k = span_of(kp[0], kp[1], a.k_rows);
     p.q_begin = q.begin;
     p.k_begin = k.begin;
     p.rows = static_cast<int>((q.end - q.begin) * a.share);
     p.keys = static_cast<int>(k.end - k.begin);
-    const int64_t at = (slot - first) * kTile;
+    const int64_t at = (slot - at_slot.first) * kTile;
     p.first = static_cast<int>(at);
     p.any = at >= 0 && at < (by_query ? p.rows : p.keys);
     return p;

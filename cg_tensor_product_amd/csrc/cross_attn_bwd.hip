@@ -288,7 +288,7 @@ struct QueryTiles {
 // The waves share tiles of keys, or with kSplitKeys (few query rows) take them in turn, as in
 // the forward.  kDelta: delta to out.delta in place of the gradient (one split).
 template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kDelta>
-__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, int64_t item, int splits, char *lds) {
+__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, uint32_t item, int splits, char *lds) {
     using C = QueryTiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32;
     const Place w = place_of<C::kRows>(a, item, true, splits, out.q_slots);
@@ -319,7 +319,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int d = 16 * s + 8 * half;
-            const bool use = row_ok && d < a.dim;
+            const bool use = row_ok && d < a.dim && t < t_end;  // a wave without keys needs no rows
             qf[s] = use ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
             gf[s] = use ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
             if (!kDelta && !out.delta && use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 :
     if (blockIdx.x < out.key_blocks)
         grad_keys<T, kDim, kDrop>(a, out, *reinterpret_cast<KeyLds<T, kDim> *>(lds));
     else
-        grad_queries<T, kDim, kDrop, kSplitKeys, false>(a, out, blockIdx.x - out.key_blocks, out.q_splits, lds);
+        grad_queries<T, kDim, kDrop, kSplitKeys, false>(a, out, blockIdx.x - static_cast<uint32_t>(out.key_blocks), out.q_splits, lds);
 }
 
 template <class T, int kDim, bool kDrop, bool kSplitKeys>

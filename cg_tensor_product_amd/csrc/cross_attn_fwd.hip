@@ -59,15 +59,6 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
     const bool row_ok = r < w.rows;
     const int64_t q_row = w.q_begin + (row_ok ? r / a.share : 0);
     const int head = w.kv_head * a.share + (row_ok ? r % a.share : 0);
-    vec8<T> qf[kSteps];
-    {
-        const T *q = static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int d = 16 * s + 8 * half;
-            qf[s] = row_ok && d < a.dim ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
-        }
-    }
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
     const uint32_t drop_row = static_cast<uint32_t>(q_row * a.heads + head);
@@ -88,6 +79,15 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
 
     int t = w.split * per + (kSplitKeys ? wave : 0);
     if (t < t_end) in.fetch(a, k_base, v_base, mask, w.keys, t);
+    vec8<T> qf[kSteps];  // a wave without keys needs none
+    {
+        const T *q = static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            qf[s] = row_ok && d < a.dim && t < t_end ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
+        }
+    }
     for (; t < t_end; t += t_step) {
         if (kSplitKeys) wave_sync();
         const uint64_t valid = in.store(k_tile, v_tile);

@@ -105,11 +105,13 @@ __device__ __forceinline__ uint32_t keep_bits(const Rng &g, uint32_t block, uint
 struct Span {
     int64_t begin, end;
 };
-__device__ __forceinline__ Span span_of(const int32_t *ptr, int b, int64_t n_rows) {
-    int64_t lo = ptr[b], hi = ptr[b + 1];
+__device__ __forceinline__ Span span_of(int64_t lo, int64_t hi, int64_t n_rows) {
     lo = lo < 0 ? 0 : lo > n_rows ? n_rows : lo;
     hi = hi < lo ? lo : hi > n_rows ? n_rows : hi;
     return {lo, hi};
+}
+__device__ __forceinline__ Span span_of(const int32_t *ptr, int b, int64_t n_rows) {
+    return span_of(int64_t(ptr[b]), int64_t(ptr[b + 1]), n_rows);
 }
 
 // Tiles of `tile` rows over ragged structures without a table of their lengths: structure
@@ -120,13 +122,19 @@ __host__ __device__ __forceinline__ int64_t tile_slots(int64_t n_rows, int n_str
     return n_rows * per / tile + n_struct;
 }
 
-// The structure that owns `slot` and the number of its first slot.  All 64 lanes of the
-// wave take part (a search with 64 probes a step) and get the same answer.
-__device__ __forceinline__ int find_structure(const int32_t *ptr, int n_struct, int per, int tile, int64_t slot,
-                                              int64_t *first) {
+// The structure that owns `slot` of the tiling by `ptr`, with its rows on both sides (`other` is
+// the second row pointer).  All 64 lanes of the wave take part (a search with 64 probes a step)
+// and get the same answer; the last step's probes bring what the answer is made of, so up to 64
+// structures take one round of loads.
+struct Owner {
+    int32_t ptr[2], other[2];  // the structure's begin and end
+    int64_t first;             // its first slot
+};
+__device__ __forceinline__ Owner find_structure(const int32_t *ptr, const int32_t *other, int n_struct, int per, int tile,
+                                                int64_t slot) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = n_struct;
-    while (n > 1) {
+    while (n > 64) {
         const int step = (n + 63) / 64;
         const int i = lane * step;
         const bool at_or_below = i < n && int64_t(ptr[lo + i]) * per / tile + (lo + i) <= slot;
@@ -135,8 +143,17 @@ __device__ __forceinline__ int find_structure(const int32_t *ptr, int n_struct, 
         lo += skip;
         n = n - skip < step ? n - skip : step;
     }
-    *first = int64_t(ptr[lo]) * per / tile + lo;
-    return lo;
+    const int i = lo + (lane < n ? lane : n - 1);
+    const int32_t p0 = ptr[i], p1 = ptr[i + 1], o0 = other[i], o1 = other[i + 1];
+    const int64_t mine = int64_t(p0) * per / tile + i;
+    const int count = __popcll(__ballot(lane < n && mine <= slot)), at = count > 1 ? count - 1 : 0;
+    Owner w;
+    w.ptr[0] = __builtin_amdgcn_readlane(p0, at);
+    w.ptr[1] = __builtin_amdgcn_readlane(p1, at);
+    w.other[0] = __builtin_amdgcn_readlane(o0, at);
+    w.other[1] = __builtin_amdgcn_readlane(o1, at);
+    w.first = int64_t(w.ptr[0]) * per / tile + (lo + at);
+    return w;
 }
 
 }  // namespace readout
