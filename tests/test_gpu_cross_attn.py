@@ -37,6 +37,9 @@ CASES = {
     "many_structures": ([1 + i % 3 for i in range(70)], [i % 9 for i in range(70)], 2, 2, 8),
     "wide_head": ([70], [90], 2, 2, 120),
     "dim_80": ([40, 7], [100, 37], 4, 2, 80),
+    "two_splits": ([150], [600], 1, 1, 48),
+    "few_states_many_rows": ([300, 5], [9, 24], 4, 1, 104),
+    "many_shared_heads": ([3, 40], [90, 33], 12, 1, 16),
 }
 
 
@@ -206,6 +209,22 @@ def test_cross_attn_of_one_state():
     assert rel_l2(host(gv), host(g).sum(0, keepdims=True)) <= RTOL["f32"]
 
 
+def test_cross_attn_gradients_of_half_types_are_near_the_rounded_result():
+    # of 96 states the rounding of out within delta is left (0.6 of the result's own at most, by
+    # its share 1 / sqrt(states in use)): sqrt(1 + 0.6^2) = 1.17, with room for the sample
+    for kind in ("bf16", "f16"):
+        r = np.random.default_rng(15)
+        q, g = (torch.from_numpy(r.normal(0, s, (64, 2, 32))).to("cuda", TYPES[kind]) for s in (1.5, 1.0))
+        k, v = (torch.from_numpy(r.normal(size=(96, 2, 32))).to("cuda", TYPES[kind]) for _ in range(2))
+        args = (index([0, 64]), index([0, 96]))
+        out, lse = oeq.oeq_cross_attn_fwd(q, k, v, *args)
+        got = oeq.oeq_cross_attn_bwd(q, k, v, *args, out, lse, g, need=("q", "k"))
+        ref = readout.cross_attn(host(q), host(k), host(v), [0, 64], [0, 96], 32 ** -0.5, grad_out=host(g))
+        for t, n in zip(got, ("grad_q", "grad_k")):
+            rounded = torch.from_numpy(ref[n]).to(TYPES[kind]).double().numpy()
+            assert rel_l2(host(t), ref[n]) <= 1.35 * rel_l2(rounded, ref[n]), n
+
+
 @pytest.mark.parametrize("need", [("q",), ("k",), ("v",), ("k", "v"), ()])
 @pytest.mark.parametrize("name", ["odd_lengths", "long_queries", "long_states"])
 def test_cross_attn_gradients_on_request(name, need):
@@ -249,6 +268,45 @@ def test_cross_attn_dropout_is_the_dropout_operators_mask():
     out, _ = oeq.oeq_cross_attn_fwd(q, v, v, index([0, 3]), index([0, Tk]), p_drop=0.4, rng=key)
     f = oeq.oeq_dropout_fwd(torch.full((3 * H, Tk), 1.0 / Tk, device="cuda"), 0.4, key)
     assert torch.allclose(out.view(3 * H, Tk), f, rtol=1e-5, atol=0)
+
+
+def test_cross_attn_of_thousands_of_structures():
+    # more than 64 x 64 structures: the search for a workgroup's structure takes three steps
+    r = np.random.default_rng(13)
+    n = 4500
+    q_len, k_len = r.integers(0, 3, n), r.integers(0, 4, n)
+    q_len[[0, -1]], k_len[[0, -1]] = 2, 3
+    qp, kp = ptr(q_len), ptr(k_len)
+    q = torch.from_numpy(r.normal(size=(qp[-1], 1, 8))).float().cuda()
+    k = torch.from_numpy(r.normal(size=(kp[-1], 1, 8))).float().cuda()
+    v = k.flip(0).contiguous()
+    g = q.flip(0).contiguous()
+    out, lse = oeq.oeq_cross_attn_fwd(q, k, v, index(qp), index(kp))
+    got = oeq.oeq_cross_attn_bwd(q, k, v, index(qp), index(kp), out, lse, g)
+    ref = readout.cross_attn(host(q), host(k), host(v), qp, kp, 8 ** -0.5, grad_out=host(g))
+    assert rel_l2(host(out), ref["out"]) <= RTOL["f32"]
+    for t, n in zip(got, ("grad_q", "grad_k", "grad_v")):
+        assert rel_l2(host(t), ref[n]) <= RTOL["f32"], n
+
+
+@pytest.mark.parametrize("lengths", [([5], [40]), ([200], [40])])
+def test_cross_attn_offsets_past_32_bits(lengths):
+    # states 2^26 elements apart: the last of 40 is 2.6e9 elements (5 GB) into the buffer
+    r = np.random.default_rng(14)
+    (nq,), (nk,) = lengths
+    stride = 1 << 26
+    buffer = torch.empty(stride * (nk - 1) + 64, dtype=torch.bfloat16, device="cuda")
+    k, v = (buffer.as_strided((nk, 1, 16), (stride, 16, 1), at) for at in (0, 16))
+    for t in (k, v):
+        t.copy_(torch.from_numpy(r.normal(size=(nk, 1, 16))))
+    q = torch.from_numpy(r.normal(size=(nq, 1, 16))).to("cuda", torch.bfloat16)
+    args = (index([0, nq]), index([0, nk]))
+    far = oeq.oeq_cross_attn_fwd(q, k, v, *args)
+    near = oeq.oeq_cross_attn_fwd(q, k.contiguous(), v.contiguous(), *args)
+    assert all(torch.equal(a, b) for a, b in zip(far, near))
+    got = oeq.oeq_cross_attn_bwd(q, k, v, *args, *far, q)
+    want = oeq.oeq_cross_attn_bwd(q, k.contiguous(), v.contiguous(), *args, *near, q)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_cross_attn_of_nothing():

@@ -252,6 +252,21 @@ def test_dropout_of_nothing():
         assert oeq.oeq_dropout_bwd(x, 0.5, state(0, 0)).shape == shape
 
 
+def test_offsets_past_32_bits():
+    # rows 2^26 elements apart: the last of 40 is 2.6e9 elements into the buffer
+    rng = np.random.default_rng(11)
+    rows, stride = 40, 1 << 26
+    x = torch.empty(stride * (rows - 1) + 32, dtype=torch.bfloat16, device="cuda").as_strided((rows, 32), (stride, 1))
+    x.copy_(rand(rng, (rows, 32), "bf16"))
+    near, p = x.contiguous(), index([0, 11, rows])
+    far = oeq.oeq_group_norm_fwd(x, p, 4, act="silu")
+    assert all(torch.equal(a, b) for a, b in zip(far, oeq.oeq_group_norm_fwd(near, p, 4, act="silu")))
+    got = oeq.oeq_group_norm_bwd(x, p, 4, far[1], far[2], near, act="silu")
+    want = oeq.oeq_group_norm_bwd(near, p, 4, far[1], far[2], near, act="silu")
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(oeq.oeq_dropout_fwd(x, 0.3, state(1, 1)), oeq.oeq_dropout_fwd(near, 0.3, state(1, 1)))
+
+
 # ---------------------------------------------------------------------------
 # both, as a program runs them
 # ---------------------------------------------------------------------------
