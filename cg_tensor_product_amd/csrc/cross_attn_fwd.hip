@@ -346,10 +346,15 @@ Choice choose(const AttnArgs &a) {
 template <class T, int kDim, bool kDrop>
 void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(c.blocks)), threads(kThreads);
+    // At 33 to 64 columns of a 16-bit type a compute unit would hold three workgroups, and with about
+    // two for each some get three and some one.  LDS that nothing uses keeps them to two there (the
+    // 512 workgroups above: 36 us for 43, with dropout 51 for 65; but 23 us for 17 where 768
+    // workgroups of 64 structures, many of them empty, can use the third place).
+    const unsigned spare = sizeof(T) == 2 && kDim == 64 && c.blocks <= 576 ? 20480 : 0;
     if (c.split_keys)
         k_forward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
     else
-        k_forward<T, kDim, kDrop, false><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
+        k_forward<T, kDim, kDrop, false><<<grid, threads, spare, stream>>>(a, c.splits, c.slots, partial);
 }
 
 template <class T, int kDim>

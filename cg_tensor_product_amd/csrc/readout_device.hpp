@@ -76,9 +76,10 @@ __device__ __forceinline__ uint4 philox(const Rng &g, uint32_t block, uint32_t r
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
-        c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+        // 0x96: the exclusive or of three words in one instruction
+        c0 = __builtin_amdgcn_bitop3_b32(uint32_t(b >> 32), c1, k0, 0x96);
         c1 = uint32_t(b);
-        c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+        c2 = __builtin_amdgcn_bitop3_b32(uint32_t(a >> 32), c3, k1, 0x96);
         c3 = uint32_t(a);
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
