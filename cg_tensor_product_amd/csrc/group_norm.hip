@@ -383,10 +383,14 @@ __device__ __forceinline__ void saved_statistics(const GroupNormArgs &a, const S
     });
 }
 
+// The second pass over the rows takes the parts in the other order: what the first read last is
+// still in the last-level cache (bf16 training step of 280000 x 256, 143 MB an operand: 261 -> 248 us).
+__device__ __forceinline__ int from_last() { return static_cast<int>(gridDim.x - 1 - blockIdx.x); }
+
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply(GroupNormArgs a, Shape s) {
-    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    const int block = from_last(), part = block / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, block - part * s.n_slabs);
     f32x8 mean, rstd;
     vec8<T> held[kStep];
     if (p.count > 0) Walk<T, kFull>(a.x, a.ld_x, p).load(held, p.count);
@@ -612,8 +616,8 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
 
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply_backward(GroupNormArgs a, Shape s, const float2 *joined) {
-    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    const int block = from_last(), part = block / s.n_slabs, b = part / s.splits;
+    const Part p = part_of(a, s, b, part - b * s.splits, block - part * s.n_slabs);
     vec8<T> hx[kStep], hg[kStep];
     hold<T, kFull>(a, p, hx, hg);
     const Channels ch(a, s, b, p);
