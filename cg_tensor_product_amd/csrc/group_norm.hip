@@ -9,16 +9,17 @@
 //   grad_x = rstd (dh - mean(dh) - xhat mean(dh xhat))
 // An empty structure has mean 0 and rstd 0.
 //
-// Everything here is bound by memory.  A workgroup owns (structure, split of its rows, slab
-// of whole groups, about 64 channels): lanes run along the channels in pieces of eight, so a
-// row of the slab is one 128- or 256-byte access, and the sums over the rows are each
-// thread's own until one reduction at the end.  Structures of few rows take one split, whose
-// workgroup computes the sums and then applies them (the second read comes from its cache);
-// with more splits the partial sums go through the workspace to a joining kernel and a third
-// one applies them.  No atomics: every result is bitwise repeatable.
+// Everything here is bound by memory.  A workgroup owns (part of a structure's rows, slab of
+// whole groups, about 64 channels): lanes run along the channels in pieces of eight, so a row of
+// the slab is one 128- or 256-byte access, and the sums over the rows are each thread's own until
+// one reduction at the end.  Structures of few rows are one part each, whose workgroup computes
+// the sums and then applies them (the second read comes from its cache); longer ones are cut into
+// tiles of rows, whose partial sums go through the workspace to a joining kernel, and a third one
+// applies them.  Tiles are as long in every structure, so the longest one sets no pace.  No
+// atomics: every result is bitwise repeatable.
 //
 // Sums are fp32 in a thread and fp64 from there on.  The variance is summed about the
-// channel's value in the split's first row, so it does not cancel against a large mean.
+// channel's value in the part's first row, so it does not cancel against a large mean.
 #include <type_traits>
 
 #include "readout.hpp"
@@ -31,8 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSlab = 64;         // channels of a slab, where a group is not wider
-constexpr int kSplitRows = 256;   // rows a split has at least, on average
-constexpr int kMostSplits = 256;
+constexpr int kWholeRows = 128;   // rows of a structure, on average, up to which it is one part
 constexpr int kStep = 4;          // rows a thread has under way
 constexpr int kJoinChannels = 8;  // channels of a workgroup that sums the weights' gradients
 
@@ -41,9 +41,17 @@ struct Shape {
     int gps;        // groups of a slab
     int n_slabs;
     int cols;       // threads along a slab's channels (a power of two)
-    int splits;
+    int tile;       // rows of a part; 0: a structure is one part
+    int64_t parts;
 };
 
+// One part a structure is two launches fewer, but goes at the longest structure's pace (SiLU, fp32,
+// forward and backward): 64 structures of 78 rows x 128 take 6.6 and 10.5 us, the like of 187 rows
+// 8.4 and 13.3, against 14.1 and 18.5 in tiles; with the same rows in uneven structures it is 87 and
+// 183 against 13.9 and 18.7.
+// The tile fills the chip once or twice over (forward and backward, fp32): 3000 rows x 128 take 11.5
+// and 13.8 us with tiles of 64 rows, 13.1 and 17.4 with 256; 100003 rows x 128 take 34.5 and 50.8
+// with 512, 37.1 and 55.9 with 256.
 Shape shape_of(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups) {
     Shape s;
     s.cg = channels / groups;
@@ -53,8 +61,13 @@ Shape shape_of(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups)
     s.gps = (groups + s.n_slabs - 1) / s.n_slabs;
     s.cols = 1;
     while (s.cols * 8 < s.gps * s.cg) s.cols *= 2;
-    int64_t splits = (rows / n_struct + kSplitRows - 1) / kSplitRows;
-    s.splits = static_cast<int>(splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits);
+    s.tile = 0;
+    s.parts = n_struct;
+    if (rows > int64_t(kWholeRows) * n_struct) {
+        const int64_t work = rows * s.n_slabs;
+        s.tile = work <= 64 * 256 ? 64 : work <= 128 * 512 ? 128 : work <= 256 * 768 ? 256 : 512;
+        s.parts = tile_slots(rows, n_struct, 1, s.tile);
+    }
     return s;
 }
 
@@ -68,29 +81,31 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// Rows [begin, end) of a structure of `len` that split i of n has.
-struct Split {
-    int begin, end;
-};
-__device__ __forceinline__ Split split_of(int len, int i, int n) {
-    const int per = static_cast<int>((static_cast<unsigned>(len) + n - 1) / static_cast<unsigned>(n));
-    const int64_t at = int64_t(per) * i, next = at + per;
-    return {at < len ? static_cast<int>(at) : len, next < len ? static_cast<int>(next) : len};
-}
-
 // What a thread works on: the channels [c, c + n) (n <= 8, none for n <= 0) of the rows
-// begin + lane, begin + lane + lanes, ..., `count` of them, of its split.
+// begin + lane, begin + lane + lanes, ..., `count` of them, of its part.
 struct Part {
+    int b;  // the structure
     int64_t begin, end;
     int c, n, lane, lanes, count, c0, width, g0, n_groups;
 };
 
-__device__ __forceinline__ Part part_of(const GroupNormArgs &a, const Shape &s, int b, int split, int slab) {
+// kTiled: part `i` is a slot of the tiling, which may be past its structure's rows (no rows then).
+template <bool kTiled>
+__device__ __forceinline__ Part part_of(const GroupNormArgs &a, const Shape &s, int i, int slab) {
     Part p;
-    const Span rows = span_of(a.ptr, b, a.rows);
-    const Split in = split_of(static_cast<int>(rows.end - rows.begin), split, s.splits);
-    p.begin = rows.begin + in.begin;
-    p.end = rows.begin + in.end;
+    if (kTiled) {
+        const Owner w = find_structure(a.ptr, a.ptr, a.n_struct, 1, s.tile, i);
+        const Span rows = span_of(w.ptr[0], w.ptr[1], a.rows);
+        const int64_t at = rows.begin + (i - w.first) * s.tile;
+        p.b = w.index;
+        p.begin = at < rows.begin || at > rows.end ? rows.end : at;
+        p.end = p.begin + s.tile < rows.end ? p.begin + s.tile : rows.end;
+    } else {
+        const Span rows = span_of(a.ptr, i, a.rows);
+        p.b = i;
+        p.begin = rows.begin;
+        p.end = rows.end;
+    }
     p.g0 = slab * s.gps;
     p.n_groups = a.groups - p.g0 < s.gps ? a.groups - p.g0 : s.gps;
     p.c0 = p.g0 * s.cg;
@@ -301,13 +316,13 @@ __device__ __forceinline__ void apply_forward(const GroupNormArgs &a, const Part
     }
 }
 
-// One split: statistics and output in one launch.
+// One part a structure: statistics and output in one launch.
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_forward(GroupNormArgs a, Shape s) {
     __shared__ Sums sums;
     __shared__ float group_mean[kSlab], group_rstd[kSlab];
     const int b = blockIdx.x / s.n_slabs;
-    const Part p = part_of(a, s, b, 0, blockIdx.x - b * s.n_slabs);
+    const Part p = part_of<false>(a, s, b, blockIdx.x - b * s.n_slabs);
     f32x8 w = channel_values(a.weight, p, 1.f), bias = channel_values(a.bias, p, 0.f), mean = {};
     vec8<T> held[kStep];
     const double n = double(p.end - p.begin) * s.cg;
@@ -327,57 +342,74 @@ __global__ void __launch_bounds__(kThreads) k_forward(GroupNormArgs a, Shape s) 
     apply_forward<T, kFull, kSilu>(a, p, held, mean, w, bias);
 }
 
-// Several splits.  partial[(b, split, group)] = {mean, sum of squared deviations}
+// Tiles of structures.  partial[(part, group)] = {mean, sum of squared deviations}
 template <class T, bool kFull>
 __global__ void __launch_bounds__(kThreads) k_statistics(GroupNormArgs a, Shape s, double2 *partial) {
     __shared__ Sums sums;
-    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    const int part = blockIdx.x / s.n_slabs;
+    const Part p = part_of<true>(a, s, part, blockIdx.x - part * s.n_slabs);
     vec8<T> held[kStep];
     statistics<T, kFull>(a, s, p, held, sums, [&](int g, double mean, double m2) {
         partial[int64_t(part) * a.groups + p.g0 + g] = make_double2(mean, m2);
     });
 }
 
-// One wave joins the splits of one (structure, group).
+// The parts of structure b: `first` and the `count` from there on, all but the last of tile rows.
+struct Parts {
+    int64_t first, count, rows;
+    __device__ __forceinline__ Parts(const GroupNormArgs &a, const Shape &s, int b) {
+        const Span span = span_of(a.ptr, b, a.rows);
+        first = int64_t(a.ptr[b]) / s.tile + b;
+        rows = span.end - span.begin;
+        count = (rows + s.tile - 1) / s.tile;
+        if (first < 0 || first + count > s.parts) count = 0;  // a row pointer that is none
+    }
+    __device__ __forceinline__ double rows_of(const Shape &s, int64_t i) const {
+        return double(i + 1 < count ? int64_t(s.tile) : rows - i * s.tile);
+    }
+};
+
+// One wave joins the parts of one (structure, group).
 __global__ void __launch_bounds__(kThreads) k_join_statistics(GroupNormArgs a, Shape s, const double2 *partial) {
     const int64_t at = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (at >= int64_t(a.n_struct) * a.groups) return;
     const int b = static_cast<int>(at / a.groups), g = static_cast<int>(at % a.groups), lane = threadIdx.x & 63;
-    const Span rows = span_of(a.ptr, b, a.rows);
-    const int len = static_cast<int>(rows.end - rows.begin);
-    const double n = double(len) * s.cg;
-    constexpr int kMine = kMostSplits / 64;
-    double2 v[kMine];
-    double k[kMine], mean = 0, m2 = 0;
+    const Parts parts(a, s, b);
+    const double2 *from = partial + parts.first * a.groups + g;
+    const double n = double(parts.rows);
+    constexpr int kHeld = 4;  // parts a lane keeps from the first walk for the second
+    double2 v[kHeld];
+    double mean = 0, m2 = 0;
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int i = lane + 64 * j;
-        v[j] = i < s.splits ? partial[(int64_t(b) * s.splits + i) * a.groups + g] : make_double2(0, 0);
-    }
+    for (int j = 0; j < kHeld; ++j) v[j] = lane + 64 * j < parts.count ? from[(lane + 64 * j) * a.groups] : make_double2(0, 0);
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const Split in = split_of(len, lane + 64 * j, s.splits);
-        k[j] = double(in.end - in.begin) * s.cg;
-        if (k[j] > 0) mean += k[j] * v[j].x;
+    for (int j = 0; j < kHeld; ++j) {
+        if (lane + 64 * j < parts.count) mean += parts.rows_of(s, lane + 64 * j) * v[j].x;
     }
+    for (int64_t i = lane + 64 * kHeld; i < parts.count; i += 64) mean += parts.rows_of(s, i) * from[i * a.groups].x;
     mean = n > 0 ? wave_sum(mean) / n : 0;
+    const auto add = [&](int64_t i, double2 part) {
+        const double off = part.x - mean;
+        m2 += part.y + parts.rows_of(s, i) * s.cg * off * off;
+    };
 #pragma unroll
-    for (int j = 0; j < kMine; ++j)
-        if (k[j] > 0) m2 += v[j].y + k[j] * (v[j].x - mean) * (v[j].x - mean);
+    for (int j = 0; j < kHeld; ++j) {
+        if (lane + 64 * j < parts.count) add(lane + 64 * j, v[j]);
+    }
+    for (int64_t i = lane + 64 * kHeld; i < parts.count; i += 64) add(i, from[i * a.groups]);
     m2 = wave_sum(m2);
     if (lane == 0) {
         a.mean[at] = static_cast<float>(mean);
-        a.rstd[at] = rstd_of(m2, n, a.eps);
+        a.rstd[at] = rstd_of(m2, n * s.cg, a.eps);
     }
 }
 
-__device__ __forceinline__ void saved_statistics(const GroupNormArgs &a, const Shape &s, int b, const Part &p,
-                                                 f32x8 *mean, f32x8 *rstd) {
+__device__ __forceinline__ void saved_statistics(const GroupNormArgs &a, const Shape &s, const Part &p, f32x8 *mean,
+                                                 f32x8 *rstd) {
     *mean = f32x8{};
     *rstd = f32x8{};
     each_group(p, s, p.c, [&](int j, int g) {
-        const int64_t at = int64_t(b) * a.groups + g;
+        const int64_t at = int64_t(p.b) * a.groups + g;
         (*mean)[j] = a.mean[at];
         (*rstd)[j] = a.rstd[at];
     });
@@ -389,12 +421,12 @@ __device__ __forceinline__ int from_last() { return static_cast<int>(gridDim.x -
 
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply(GroupNormArgs a, Shape s) {
-    const int block = from_last(), part = block / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, block - part * s.n_slabs);
+    const int block = from_last(), part = block / s.n_slabs;
+    const Part p = part_of<true>(a, s, part, block - part * s.n_slabs);
     f32x8 mean, rstd;
     vec8<T> held[kStep];
     if (p.count > 0) Walk<T, kFull>(a.x, a.ld_x, p).load(held, p.count);
-    saved_statistics(a, s, b, p, &mean, &rstd);
+    saved_statistics(a, s, p, &mean, &rstd);
     const f32x8 w = channel_values(a.weight, p, 1.f) * rstd, bias = channel_values(a.bias, p, 0.f);
     apply_forward<T, kFull, kSilu>(a, p, held, mean, w, bias);
 }
@@ -404,8 +436,8 @@ __global__ void __launch_bounds__(kThreads) k_apply(GroupNormArgs a, Shape s) {
 // What a thread needs of its channels; z = (x - mean) scale + bias with scale = rstd w.
 struct Channels {
     f32x8 mean, rstd, scale, bias;
-    __device__ __forceinline__ Channels(const GroupNormArgs &a, const Shape &s, int b, const Part &p) {
-        saved_statistics(a, s, b, p, &mean, &rstd);
+    __device__ __forceinline__ Channels(const GroupNormArgs &a, const Shape &s, const Part &p) {
+        saved_statistics(a, s, p, &mean, &rstd);
         scale = channel_values(a.weight, p, 1.f) * rstd;
         bias = channel_values(a.bias, p, 0.f);
     }
@@ -523,10 +555,10 @@ __global__ void __launch_bounds__(kThreads) k_backward(GroupNormArgs a, Shape s,
     __shared__ Sums sums;
     __shared__ float group_m1[kSlab], group_m2[kSlab];
     const int b = blockIdx.x / s.n_slabs;
-    const Part p = part_of(a, s, b, 0, blockIdx.x - b * s.n_slabs);
+    const Part p = part_of<false>(a, s, b, blockIdx.x - b * s.n_slabs);
     vec8<T> hx[kStep], hg[kStep];
     hold<T, kFull>(a, p, hx, hg);
-    const Channels ch(a, s, b, p);
+    const Channels ch(a, s, p);
     const double n = double(p.end - p.begin) * s.cg;
     gradient_sums<T, kFull, kSilu>(a, s, p, b, ch, hx, hg, column, sums, [&](int g, double dh, double dhx) {
         group_m1[g] = n > 0 ? static_cast<float>(dh / n) : 0.f;
@@ -545,17 +577,17 @@ __global__ void __launch_bounds__(kThreads) k_backward(GroupNormArgs a, Shape s,
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_gradient_sums(GroupNormArgs a, Shape s, float *column, double2 *partial) {
     __shared__ Sums sums;
-    const int part = blockIdx.x / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, blockIdx.x - part * s.n_slabs);
+    const int part = blockIdx.x / s.n_slabs;
+    const Part p = part_of<true>(a, s, part, blockIdx.x - part * s.n_slabs);
     vec8<T> hx[kStep], hg[kStep];
     hold<T, kFull>(a, p, hx, hg);
-    const Channels ch(a, s, b, p);
+    const Channels ch(a, s, p);
     gradient_sums<T, kFull, kSilu>(a, s, p, part, ch, hx, hg, column, sums, [&](int g, double dh, double dhx) {
         partial[int64_t(part) * a.groups + p.g0 + g] = make_double2(dh, dhx);
     });
 }
 
-// The first `join_blocks` workgroups join the splits' group sums to means (one wave a
+// The first `join_blocks` workgroups join the parts' group sums to means (one wave a
 // (structure, group)); the others sum `column` over its rows, kJoinChannels a workgroup.
 __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Shape s, const double2 *partial,
                                                              float2 *joined, const float *column, int join_blocks) {
@@ -563,11 +595,11 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
         const int64_t at = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
         if (at >= int64_t(a.n_struct) * a.groups) return;
         const int b = static_cast<int>(at / a.groups), g = static_cast<int>(at % a.groups), lane = threadIdx.x & 63;
-        const Span rows = span_of(a.ptr, b, a.rows);
-        const double n = double(rows.end - rows.begin) * s.cg;
+        const Parts parts(a, s, b);
+        const double n = double(parts.rows) * s.cg;
         double u = 0, v = 0;
-        for (int i = lane; i < s.splits; i += 64) {
-            const double2 t = partial[(int64_t(b) * s.splits + i) * a.groups + g];
+        for (int64_t i = lane; i < parts.count; i += 64) {
+            const double2 t = partial[(parts.first + i) * a.groups + g];
             u += t.x;
             v += t.y;
         }
@@ -581,7 +613,7 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
     constexpr int kLanes = kThreads / kJoinChannels, kAhead = 8;
     const int col = threadIdx.x % kJoinChannels, lane = threadIdx.x / kJoinChannels;
     const int c = (blockIdx.x - join_blocks) * kJoinChannels + col;
-    const int n_parts = a.n_struct * s.splits;
+    const int n_parts = static_cast<int>(s.parts);
     double u = 0, v = 0;
     if (c < a.channels) {
         for (int r = lane; r < n_parts; r += kLanes * kAhead) {
@@ -616,14 +648,14 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
 
 template <class T, bool kFull, bool kSilu>
 __global__ void __launch_bounds__(kThreads) k_apply_backward(GroupNormArgs a, Shape s, const float2 *joined) {
-    const int block = from_last(), part = block / s.n_slabs, b = part / s.splits;
-    const Part p = part_of(a, s, b, part - b * s.splits, block - part * s.n_slabs);
+    const int block = from_last(), part = block / s.n_slabs;
+    const Part p = part_of<true>(a, s, part, block - part * s.n_slabs);
     vec8<T> hx[kStep], hg[kStep];
     hold<T, kFull>(a, p, hx, hg);
-    const Channels ch(a, s, b, p);
+    const Channels ch(a, s, p);
     f32x8 m1 = {}, m2 = {};
     each_group(p, s, p.c, [&](int j, int g) {
-        const float2 t = joined[int64_t(b) * a.groups + g];
+        const float2 t = joined[int64_t(p.b) * a.groups + g];
         m1[j] = t.x;
         m2[j] = t.y;
     });
@@ -632,16 +664,16 @@ __global__ void __launch_bounds__(kThreads) k_apply_backward(GroupNormArgs a, Sh
 
 constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace pieces: the splits' group sums, the joined means of the backward, the channel sums.
+// Workspace pieces: the parts' group sums, the joined means of the backward, the channel sums.
 struct Pieces {
     size_t partial, joined, column, bytes;
 };
 Pieces pieces_of(const Shape &s, int32_t n_struct, int32_t channels, int32_t groups) {
     Pieces w;
-    const size_t parts = static_cast<size_t>(n_struct) * s.splits;
+    const size_t parts = static_cast<size_t>(s.parts);
     w.partial = 0;
-    w.joined = w.partial + (s.splits > 1 ? up(parts * groups * sizeof(double2)) : 0);
-    w.column = w.joined + (s.splits > 1 ? up(static_cast<size_t>(n_struct) * groups * sizeof(float2)) : 0);
+    w.joined = w.partial + (s.tile ? up(parts * groups * sizeof(double2)) : 0);
+    w.column = w.joined + (s.tile ? up(static_cast<size_t>(n_struct) * groups * sizeof(float2)) : 0);
     w.bytes = w.column + up(parts * channels * 2 * sizeof(float));
     return w;
 }
@@ -649,8 +681,8 @@ Pieces pieces_of(const Shape &s, int32_t n_struct, int32_t channels, int32_t gro
 template <class T, bool kFull, bool kSilu>
 hipError_t forward(const GroupNormArgs &a, hipStream_t stream) {
     const Shape s = shape_of(a.rows, a.n_struct, a.channels, a.groups);
-    const dim3 grid(static_cast<unsigned>(int64_t(a.n_struct) * s.splits * s.n_slabs)), threads(kThreads);
-    if (s.splits == 1) {
+    const dim3 grid(static_cast<unsigned>(s.parts * s.n_slabs)), threads(kThreads);
+    if (!s.tile) {
         k_forward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s);
         return hipGetLastError();
     }
@@ -678,8 +710,8 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t stream) {
     double2 *partial = reinterpret_cast<double2 *>(ws + w.partial);
     float2 *joined = reinterpret_cast<float2 *>(ws + w.joined);
     float *column = params ? reinterpret_cast<float *>(ws + w.column) : nullptr;
-    const dim3 grid(static_cast<unsigned>(int64_t(a.n_struct) * s.splits * s.n_slabs));
-    if (s.splits == 1) {
+    const dim3 grid(static_cast<unsigned>(s.parts * s.n_slabs));
+    if (!s.tile) {
         k_backward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, column);
         if (params) k_join_gradients<<<dim3(channel_blocks), threads, 0, stream>>>(a, s, partial, joined, column, 0);
         return hipGetLastError();
@@ -725,7 +757,7 @@ GroupNormBytes group_norm_workspace(int64_t rows, int32_t n_struct, int32_t chan
 
 int64_t group_norm_blocks(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups) {
     const Shape s = shape_of(rows, n_struct, channels, groups);
-    return int64_t(n_struct) * s.splits * s.n_slabs;
+    return s.parts * s.n_slabs;
 }
 
 hipError_t group_norm_fwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream) {

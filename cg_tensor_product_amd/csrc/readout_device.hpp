@@ -129,6 +129,7 @@ __host__ __device__ __forceinline__ int64_t tile_slots(int64_t n_rows, int n_str
 // structures take one round of loads.
 struct Owner {
     int32_t ptr[2], other[2];  // the structure's begin and end
+    int index;                 // which it is
     int64_t first;             // its first slot
 };
 __device__ __forceinline__ Owner find_structure(const int32_t *ptr, const int32_t *other, int n_struct, int per, int tile,
@@ -153,6 +154,7 @@ __device__ __forceinline__ Owner find_structure(const int32_t *ptr, const int32_
     w.ptr[1] = __builtin_amdgcn_readlane(p1, at);
     w.other[0] = __builtin_amdgcn_readlane(o0, at);
     w.other[1] = __builtin_amdgcn_readlane(o1, at);
+    w.index = lo + at;
     w.first = int64_t(w.ptr[0]) * per / tile + (lo + at);
     return w;
 }

@@ -84,6 +84,37 @@ def test_group_norm(name, act, kind):
         assert np.abs(host(gx)).max() <= 1e-3 and np.abs(host(gw)).max() <= 1e-3
 
 
+# structures cut into tiles of 64, 128, 256 and 512 rows: ends on a tile, one row past it and one
+# short of it, a structure that has almost all the rows, over 64 structures, rows before the first
+TILED = {
+    "tiles_of_64": ([0, 64, 193, 320, 383, 1000, 1000], 24, 3),
+    "tiles_of_128": ([0, 1, 129, 257, 40000], 12, 3),
+    "tiles_of_256": ([0, 256, 256, 99000, 99257, 99512], 16, 2),
+    "tiles_of_512": ([0, 512, 1025, 200000], 8, 1),
+    "many_in_tiles": ([17 + 150 * i + (i * i) % 97 for i in range(131)], 40, 4),
+}
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(TILED))
+def test_group_norm_in_tiles(name, kind):
+    ptr, C, G = TILED[name]
+    rng = np.random.default_rng(700 + len(name))
+    x, g = rand(rng, (ptr[-1], C), kind, 1.5, 0.5), rand(rng, (ptr[-1], C), kind)
+    w, b = rand(rng, (C,), "f32", 0.3, 1.0), rand(rng, (C,), "f32", 0.3)
+    p = index(ptr)
+    out, mean, rstd = oeq.oeq_group_norm_fwd(x, p, G, w, b, act="silu")
+    gx, gw, gb = oeq.oeq_group_norm_bwd(x, p, G, mean, rstd, g, w, b, act="silu")
+    ref = readout.group_norm(host(x), ptr, G, host(w), host(b), act="silu", grad_out=host(g))
+    rows = slice(ptr[0], ptr[-1])  # rows of no structure are not written
+    assert rel_l2(host(mean), ref["mean"]) <= RTOL["f32"]
+    assert rel_l2(host(rstd), ref["rstd"]) <= RTOL["f32"]
+    assert rel_l2(host(out)[rows], ref["out"][rows]) <= bound(kind)
+    assert rel_l2(host(gx)[rows], ref["grad_x"][rows]) <= bound(kind)
+    assert rel_l2(host(gw), ref["grad_weight"]) <= RTOL["f32"]
+    assert rel_l2(host(gb), ref["grad_bias"]) <= RTOL["f32"]
+
+
 def test_group_norm_without_weight_and_bias():
     rng = np.random.default_rng(1)
     ptr = [0, 7, 30]
