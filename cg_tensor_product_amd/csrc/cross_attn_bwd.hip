@@ -9,10 +9,15 @@
 //   grad_queries  a wave owns 32 query rows and walks the keys, like the forward.
 // Both form delta themselves, from rows that they read anyway and from out.  Where out is
 // rounded to 16 bits and the structures have few states (kExactStates), that rounding would be
-// most of the gradients' error: there a pass of its own sums p dp in fp32 first.  Scores are formed twice (7 products of the minimal 5); the alternative, one walk
-// that adds into grad_q, needs atomics or a partial grad_q for each tile of keys.  With few
-// workgroups the walks are split over workgroups, whose fp32 partial sums a second kernel adds
-// in order.
+// most of the gradients' error: there a pass of its own sums p dp in fp32 first.
+// Scores are formed twice (7 products of the minimal 5; 9 for 16-bit types with the second term of
+// the score gradients); the alternative, one walk that adds into grad_q, needs atomics or a partial
+// grad_q for each tile of keys.  With few workgroups the walks are split over workgroups, whose
+// fp32 partial sums a second kernel adds in order.
+//
+// Bound by the vector unit next to the matrix unit, fp32 by its matrix instructions: 4 structures of
+// 1024 query rows and 2048 states, 8 heads over 4, D = 64: bf16 115 us (373 TFLOP/s of the minimal
+// products; 144 us with dropout, whose generator runs in both roles), fp32 483 us (89 TFLOP/s).
 //
 // The product that gives dp starts from -delta / (factor of what is kept) in its accumulators,
 // so that a score's gradient is one multiplication, and the factor is applied to the sums.
@@ -32,7 +37,8 @@ constexpr int kExactStates = 32;
 // The score gradients of 16-bit types go into their products as two terms, the rounded value and
 // the rest: rounded once, they and delta's rounding leave grad_q and grad_k with 1.4 to 1.9 times
 // the error that rounding the result alone does (10 to 4096 states), with the rest 1.0 to 1.2 from
-// 64 states on.  It costs 7 % of a decoder's training step (224 -> 239 us).
+// 64 states on.  It costs 7 % of a decoder's training step (8 structures of up to 1024 query rows and
+// 2048 states, 8 heads over 4, D = 64, bf16, dropout: 224 -> 239 us).
 template <class T>
 constexpr bool kRest = sizeof(T) == 2;
 
@@ -442,7 +448,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 }
 
 // Two workgroups a compute unit, where that does not leave too few registers: against one, D = 96
-// takes 166 us for 279 and D = 128 239 for 328 (bf16, 4 structures of 1024 query rows and 2048
+// takes 165 us for 279 and D = 128 239 for 328 (bf16, 4 structures of 1024 query rows and 2048
 // states, 8 heads over 4); fp32 at D = 128 would take 1369 for 1102.
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
 __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 : 1) k_backward(AttnArgs a, Bwd out) {

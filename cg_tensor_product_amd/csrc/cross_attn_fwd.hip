@@ -13,6 +13,13 @@
 //          and take tiles of 32 keys in turn, each through LDS of its own and without
 //          barriers; their results are joined in LDS at the end.
 // With few workgroups the keys are also split over workgroups; a second kernel joins them.
+//
+// Large calls are bound by the vector unit (exponentials, the running maximum, the copies of the
+// output's rescaling) next to the matrix unit: fp16, 2 x 2048 query rows x 16 heads over 5000
+// states, D = 128: 200 us, 840 TFLOP/s; with D = 64 bf16 at 485 TFLOP/s, where an exponential is
+// worth half the products.  fp32 runs at the rate of its matrix instructions (115 TFLOP/s, D = 64).
+// Single tokens are bound by the read of K and V: 16 x up to 5000 states, 4 key heads of 64, bf16,
+// 15 us and 4 for the join.
 #include "attn_device.hpp"
 
 namespace oeq {
@@ -332,8 +339,8 @@ Choice choose(const AttnArgs &a) {
     c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
     // Splits until the workgroups fill the chip about once (256 compute units; four workgroups each
     // at D <= 32, else two).  4 structures of 1024 query rows and 2048 states, 8 heads over 4:
-    // bf16, D = 64 takes 40 us with 512 workgroups, 49 with 768 and 45 with 1024; D = 32 takes
-    // 39, 37 and 34 us; fp32, D = 128 takes 305, 400 and 324 us.
+    // bf16, D = 64 takes 36 us with 512 workgroups, 49 with 768 and 45 with 1024; D = 32 takes
+    // 39, 37 and 31 us; fp32, D = 128 takes 303, 400 and 324 us.
     const int64_t fill = 256 * (a.dim <= 32 ? 4 : 2);
     const int64_t base = c.slots * a.kv_heads, most = a.k_rows / a.n_struct / 256;  // 256 keys a split at least
     int64_t splits = (fill + base / 2) / base;

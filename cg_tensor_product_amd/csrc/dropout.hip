@@ -3,8 +3,9 @@
 // column) and is formed again wherever it is needed, so nothing but the operands moves.
 //
 // One thread takes the eight columns of one generator block: 16-byte loads of 16-bit types,
-// two of them of fp32.  Bound by memory for fp32 and by memory and the generator's multiplies
-// together for 16-bit types.
+// two of them of fp32, so a block's ten rounds serve all its columns.  Bound by memory: 280000 x
+// 256, bf16, 49 us (5.8 TB/s, the copy rate, with the vector unit two thirds busy); 5000 x 1152,
+// fp32, with a residual 11.9 us.
 #include <type_traits>
 
 #include "readout.hpp"

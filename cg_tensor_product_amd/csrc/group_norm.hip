@@ -18,6 +18,10 @@
 // applies them.  Tiles are as long in every structure, so the longest one sets no pace.  No
 // atomics: every result is bitwise repeatable.
 //
+// 280000 x 256 in 32 uneven structures, bf16, SiLU (143 MB an operand): statistics 40 us, output 52
+// (5.5 TB/s), gradient sums 67 (4.3 TB/s, the vector unit three quarters busy), grad_x 77 (5.6 TB/s);
+// 100003 x 128, fp32: 12.9 and 18.7 us.  A few molecules are one kernel of 5 us, its loads' latency.
+//
 // Sums are fp32 in a thread and fp64 from there on.  The variance is summed about the
 // channel's value in the part's first row, so it does not cancel against a large mean.
 #include <type_traits>
@@ -416,7 +420,7 @@ __device__ __forceinline__ void saved_statistics(const GroupNormArgs &a, const S
 }
 
 // The second pass over the rows takes the parts in the other order: what the first read last is
-// still in the last-level cache (bf16 training step of 280000 x 256, 143 MB an operand: 261 -> 248 us).
+// still in the last-level cache (bf16 training step of 280000 x 256, 143 MB an operand: 261 -> 248 us, 240 in tiles).
 __device__ __forceinline__ int from_last() { return static_cast<int>(gridDim.x - 1 - blockIdx.x); }
 
 template <class T, bool kFull, bool kSilu>
