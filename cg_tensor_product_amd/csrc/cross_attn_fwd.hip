@@ -50,6 +50,26 @@ struct Partial {
     float *lse;  // [split][query row, head], in powers of two
 };
 
+// f(i, v) with a lane's results of a 32 x 32 block as eight consecutive rows of it from 8 i on (the
+// two halves exchange theirs), so that a lane writes 16 bytes of a 16-bit type at once, not 8: 40 x 450
+// query rows x 16 heads over 9 states each, D = 80, bf16, 37 -> 33 us.  Lanes l and l + 32 have to be
+// active together.
+template <class F>
+__device__ __forceinline__ void each_eight(f32x16 o, int half, F &&f) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        f32x8 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(o[4 * i + j]), __float_as_uint(o[4 * i + 4 + j]),
+                                                            false, false);
+            v[j] = __uint_as_float(r[0]);
+            v[4 + j] = __uint_as_float(r[1]);
+        }
+        f(i + half, v);
+    }
+}
+
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
 __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, int64_t slots, Partial partial) {
     using C = Tiles<T, kDim, kSplitKeys>;
@@ -180,14 +200,9 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
             if (half == 0) partial.lse[to] = lse2;
 #pragma unroll
             for (int d = 0; d < kOut; ++d) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = 32 * d + 8 * i + 4 * half;
-                    if (col < a.dim) {
-                        const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-                        *reinterpret_cast<f32x4 *>(partial.out + to * a.dim + col) = v * norm;
-                    }
-                }
+                each_eight(o[d], half, [&](int i, f32x8 v) {
+                    if (32 * d + 8 * i < a.dim) store8(partial.out + to * a.dim + 32 * d + 8 * i, v * norm);
+                });
             }
             return;
         }
@@ -195,15 +210,9 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
         T *out = static_cast<T *>(a.out) + at * a.dim;
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = 32 * d + 8 * i + 4 * half;
-                if (col < a.dim) {
-                    using V4 = T __attribute__((ext_vector_type(4)));
-                    const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-                    *reinterpret_cast<V4 *>(out + col) = __builtin_convertvector(v * norm, V4);
-                }
-            }
+            each_eight(o[d], half, [&](int i, f32x8 v) {
+                if (32 * d + 8 * i < a.dim) store8(out + 32 * d + 8 * i, from_f32<T>(v * norm));
+            });
         }
         return;
     }
