@@ -85,6 +85,10 @@ def _like(t, x, dev, name):
 def _scratch(nbytes, workspace, device):
     """(tensor to keep, address, bytes): the caller's workspace, or a 256-byte aligned one."""
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != device:
+            raise TypeError(f"workspace must be a tensor on device {device}")
+        if not workspace.is_contiguous():  # else it may own fewer bytes than it counts
+            raise ValueError("workspace must be contiguous")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, None, 0
