@@ -466,24 +466,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_delta(AttnArgs a, Bwd out) {
     grad_queries<T, kDim, kDrop, kSplitKeys, true>(a, out, blockIdx.x, 1, lds);
 }
 
-// out = sum of `splits` fp32 arrays of n values (a multiple of eight), in order; up to three.
+// out = sum of `splits` fp32 arrays of `rows` rows of `row` values (a multiple of eight), in order, for
+// the rows that the structures of `ptr` hold (the others have no partial sums and are not written); up
+// to three.
 struct Sum {
     const float *part;
     void *out;
-    int64_t n;
+    const int32_t *ptr;
+    int64_t rows, row;  // row = 0: nothing to do
     int splits;
 };
 struct Sums {
     Sum job[3];
+    int32_t n_struct;
 };
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_add(Sums sums) {
     const int64_t step = int64_t(gridDim.x) * kThreads * 8;
     for (const Sum &j : sums.job) {
-        for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < j.n; i += step) {
+        const Span held = span_of(j.ptr[0], j.ptr[sums.n_struct], j.rows);
+        const int64_t n = j.rows * j.row, end = held.end * j.row;
+        for (int64_t i = held.begin * j.row + (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < end; i += step) {
             f32x8 v = load8(j.part + i);
 #pragma unroll 8
-            for (int s = 1; s < j.splits; ++s) v += load8(j.part + s * j.n + i);
+            for (int s = 1; s < j.splits; ++s) v += load8(j.part + s * n + i);
             store8(static_cast<T *>(j.out) + i, from_f32<T>(v));
         }
     }
@@ -571,11 +577,13 @@ hipError_t backward(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
         launch<T, 96>(a, c, out, blocks, stream);
     else
         launch<T, 128>(a, c, out, blocks, stream);
-    const int64_t nq = a.grad_q && c.q_splits > 1 ? a.q_rows * a.heads * a.dim : 0;
-    const int64_t nk = c.k_splits > 1 ? a.k_rows * a.kv_heads * a.dim : 0;
-    const Sums sums = {{{out.part_q, a.grad_q, nq, c.q_splits},
-                        {out.part_k, a.grad_k, a.grad_k ? nk : 0, c.k_splits},
-                        {out.part_v, a.grad_v, a.grad_v ? nk : 0, c.k_splits}}};
+    const int64_t q_row = a.grad_q && c.q_splits > 1 ? int64_t(a.heads) * a.dim : 0;
+    const int64_t k_row = c.k_splits > 1 ? int64_t(a.kv_heads) * a.dim : 0;
+    const Sums sums = {{{out.part_q, a.grad_q, a.q_ptr, a.q_rows, q_row, c.q_splits},
+                        {out.part_k, a.grad_k, a.k_ptr, a.k_rows, a.grad_k ? k_row : 0, c.k_splits},
+                        {out.part_v, a.grad_v, a.k_ptr, a.k_rows, a.grad_v ? k_row : 0, c.k_splits}},
+                       a.n_struct};
+    const int64_t nq = a.q_rows * q_row, nk = a.grad_k || a.grad_v ? a.k_rows * k_row : 0;
     const int64_t most = nq > nk ? nq : nk, grid = (most / 8 + kThreads - 1) / kThreads;
     if (most)
         k_add<T><<<dim3(static_cast<unsigned>(grid > 4096 ? 4096 : grid)), dim3(kThreads), 0, stream>>>(sums);

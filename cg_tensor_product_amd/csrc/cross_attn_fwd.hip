@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Parti
     constexpr int kAhead = 4, kRow = kLanes * kGroups;
     const int64_t n = a.q_rows * a.heads, at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kRow;
     const int col = threadIdx.x % kLanes * 8, group = threadIdx.x % kRow / kLanes;
-    if (at >= n) return;  // whole rows of threads: the exchanges below stay within one
+    // Rows that no structure holds have no partial results and are not written.  Whole rows of threads
+    // end here: the exchanges below stay within one.
+    const Span held = span_of(a.q_ptr[0], a.q_ptr[a.n_struct], a.q_rows);
+    if (at < held.begin * a.heads || at >= held.end * a.heads) return;
     float most = -INFINITY, total = 0.f, bad = 0.f;
     f32x8 v = {};
     for (int first = group; first < splits; first += kGroups * kAhead) {
