@@ -211,6 +211,11 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(q_tile, kRow, row, 16 * i, half), kf[i]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(g_tile, kRow, row, 16 * i, half), vf[i]);
+        if (!whole) {
+            // the zeros that stand for rows past the end give NaN against an infinite state
+            rare();
+            each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
+        }
         vec8<T> pf[2], sf[2], sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

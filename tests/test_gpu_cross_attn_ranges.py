@@ -83,3 +83,22 @@ def test_rows_of_no_structure_are_not_written(first, q_end, k_end, q_rows, k_row
     assert rel_l2(host(out[held_q]), ref["out"]) <= 2 * u + RTOL["f32"]
     for t, n, held in zip(grads, ("grad_q", "grad_k", "grad_v"), (held_q, held_k, held_k)):
         assert rel_l2(host(t[held]), ref[n]) <= 4 * u + RTOL["f32"], n
+
+
+# ---- infinite states ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("q_len,k_len", [([5], [20]), ([33, 1], [70, 200]), ([1], [9]), ([129], [40])])
+def test_gradients_of_states_with_minus_infinite_scores(q_len, k_len, kind):
+    # every other visible state has the score -infinity for every row, so a probability of zero: its
+    # gradients are zero and the other states' are what they would be without it.  (grad_q takes
+    # zero times the infinite state, which is NaN in the formula too.)
+    q, k, v, g = operands(kind, q_len, k_len, 2, 1, 32, 37)
+    q = q.abs() + 0.125
+    k[::2] = -float("inf")
+    got, ref = both(q, k, v, g, q_len, k_len)
+    u = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    assert rel_l2(host(got["out"]), ref["out"]) <= 2 * u + RTOL["f32"]
+    for n in ("grad_k", "grad_v"):
+        assert torch.all(got[n][::2] == 0), n
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
