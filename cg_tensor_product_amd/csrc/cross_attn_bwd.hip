@@ -166,8 +166,6 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 
     for (int buffer = 0; t < t_end; ++t, buffer ^= 1) {
         const int r0 = t * kRowTile, in_tile = min(kRowTile, w.rows - r0);
-        const bool whole = in_tile == kRowTile;
-        const uint64_t valid = (1ull << in_tile) - 1;
         T *q_tile = lds.q[buffer], *g_tile = lds.g[buffer];
         if (out.delta) {
             if (threadIdx.x < kRowTile)
@@ -182,9 +180,10 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
                 if (q_in.d == 0 && row < kRowTile) lds.delta[buffer][row] = row < in_tile ? v * start : 0.f;
             }
         }
-        q_in.store(q_tile, whole, valid);
-        g_in.store(g_tile, whole, valid);
-        // rows past the end count as rows that saw nothing
+        // Rows past the end are the last one again, as a row that saw nothing: their probabilities are
+        // zero, and NaN only where the last row's are (zeros would give NaN against an infinite state).
+        q_in.store(q_tile, true, 0);
+        g_in.store(g_tile, true, 0);
         if (threadIdx.x < kRowTile) lds.lse[buffer][threadIdx.x] = static_cast<int>(threadIdx.x) < in_tile ? kept_lse<T>(lse_in) : INFINITY;
         if (kDrop) {
             // 32 rows x 4 generator blocks of this wave's keys, two a lane; a row's bits make a word
@@ -211,11 +210,6 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(q_tile, kRow, row, 16 * i, half), kf[i]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(g_tile, kRow, row, 16 * i, half), vf[i]);
-        if (!whole) {
-            // the zeros that stand for rows past the end give NaN against an infinite state
-            rare();
-            each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
-        }
         vec8<T> pf[2], sf[2], sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
