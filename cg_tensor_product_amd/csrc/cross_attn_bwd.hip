@@ -8,8 +8,8 @@
 //                 the sum over shared heads needs no further step;
 //   grad_queries  a wave owns 32 query rows and walks the keys, like the forward.
 // Both form delta themselves, from rows that they read anyway and from out.  Where out is
-// rounded to 16 bits and the structures have few states (kExactStates), that rounding would be
-// most of the gradients' error: there a pass of its own sums p dp in fp32 first.
+// rounded to 16 bits and a structure has few states (kExactStates), that rounding would be
+// most of its gradients' error: there, in one tile of keys, delta is the sum of p dp in fp32.
 // Scores are formed twice (7 products of the minimal 5; 9 for 16-bit types with the second term of
 // the score gradients); the alternative, one walk that adds into grad_q, needs atomics or a partial
 // grad_q for each tile of keys.  With few workgroups the walks are split over workgroups, whose
@@ -32,7 +32,13 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kKeyTile = 128;  // keys of a workgroup that owns keys
 constexpr int kRowTile = 32;   // query rows of a step of its walk
+// Structures of so many states, one tile of one wave, sum p dp for delta.  From the rounded out instead,
+// grad_q and grad_k have 3.0 times the error that rounding the result has at 2 states, 2.1 at 4, 1.7 at
+// 8, 1.3 at 32 and 1.2 at 64 (1.0 from p dp).  It goes by each structure's length, so its gradients do not
+// depend on what else is in its batch.
 constexpr int kExactStates = 32;
+template <class T>
+constexpr bool kExactDelta = sizeof(T) == 2;
 
 // The score gradients of 16-bit types go into their products as two terms, the rounded value and
 // the rest: rounded once, they and delta's rounding leave grad_q and grad_k with 1.4 to 1.9 times
@@ -43,7 +49,6 @@ template <class T>
 constexpr bool kRest = sizeof(T) == 2;
 
 struct Bwd {
-    float *delta;  // [query row, head]: -delta / factor of what is kept, or NULL: formed from out
     float *part_q;           // [split][query row, head][dim]
     float *part_k, *part_v;  // [split][key, key head][dim]
     int q_splits, k_splits;  // 1: gradients are written directly
@@ -97,11 +102,24 @@ struct KeyLds {
     uint32_t kept[kWaves][kRowTile];             // bit = key of the wave
 };
 
-template <class T, int kDim, bool kDrop>
-__device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, KeyLds<T, kDim> &lds) {
+// Sum over the 32 lanes of a half: sixteen by rotations, then both sixteens.
+__device__ __forceinline__ float sum_half(float v) {
+    const auto rotated = [](float x, auto by) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + decltype(by)::value, 0xF, 0xF, true));
+    };
+    v += rotated(v, std::integral_constant<int, 8>());
+    v += rotated(v, std::integral_constant<int, 4>());
+    v += rotated(v, std::integral_constant<int, 2>());
+    v += rotated(v, std::integral_constant<int, 1>());
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// kExact: the structure has kExactStates keys at most, all of them in the first wave, which forms delta
+// from p dp; the other waves only bring rows.
+template <class T, int kDim, bool kDrop, bool kExact>
+__device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, const Place &w, KeyLds<T, kDim> &lds) {
     constexpr int kRow = KeyLds<T, kDim>::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const Place w = place_of<kKeyTile>(a, blockIdx.x, false, out.k_splits, out.k_slots);
-    if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int key = w.first + wave * 32 + (lane & 31);
     const bool key_ok = key < w.keys;
@@ -110,7 +128,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 
     using Stage = RowStage<T, kRowTile, kDim, kThreads>;
     Stage q_in(threadIdx.x, a.dim), g_in(threadIdx.x, a.dim), o_in(threadIdx.x, a.dim);
-    float lse_in = 0.f, delta_in = 0.f;
+    float lse_in = 0.f;
     const int n_tiles = (w.rows + kRowTile - 1) / kRowTile, per = (n_tiles + out.k_splits - 1) / out.k_splits;
     const int t_end = min(n_tiles, (w.split + 1) * per);
     const auto row_of = [&](int r, int64_t *q_row) {  // rows past the end: the last one
@@ -134,14 +152,13 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
 #pragma unroll
             for (int i = 0; i < Stage::kPieces; ++i) {
                 g_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.grad_out) + at[i]);
-                if (!out.delta) o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
+                if (!kExact) o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
             }
         }
         if (threadIdx.x < kRowTile) {
             int64_t q_row;
             const int r = t * kRowTile + threadIdx.x, head = row_of(r, &q_row);
             lse_in = a.lse[q_row * a.heads + head];
-            if (out.delta) delta_in = out.delta[q_row * a.heads + head];
         }
     };
     int t = w.split * per;
@@ -167,10 +184,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
     for (int buffer = 0; t < t_end; ++t, buffer ^= 1) {
         const int r0 = t * kRowTile, in_tile = min(kRowTile, w.rows - r0);
         T *q_tile = lds.q[buffer], *g_tile = lds.g[buffer];
-        if (out.delta) {
-            if (threadIdx.x < kRowTile)
-                lds.delta[buffer][threadIdx.x] = static_cast<int>(threadIdx.x) < in_tile ? delta_in : 0.f;
-        } else {
+        if (!kExact) {
 #pragma unroll
             for (int i = 0; i < Stage::kPieces; ++i) {
                 const int row = q_in.row + i * Stage::kStep;
@@ -197,10 +211,11 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
         }
         __syncthreads();
         fetch(min(t + 1, t_end - 1));  // at the end, again the last
+        if (kExact && wave > 0) continue;
 
-        f32x16 s = {}, dp;
+        f32x16 s = {}, dp = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4 && !kExact; ++i) {
             const f32x4 d = *reinterpret_cast<const f32x4 *>(lds.delta[buffer] + 16 * (i >> 1) + 8 * half + 4 * (i & 1));
 #pragma unroll
             for (int j = 0; j < 4; ++j) dp[4 * i + j] = d[j];
@@ -221,7 +236,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
             f32x8 p8, s8, lse = load_lds8(lds.lse[buffer] + first), none;
             uint32_t kept[8];
             if (kDrop) {
-                none = load_lds8(lds.delta[buffer] + first);
+                if (!kExact) none = load_lds8(lds.delta[buffer] + first);
                 const uint4 *from = reinterpret_cast<const uint4 *>(lds.kept[wave] + first);
                 const uint4 x = from[0], y = from[1];
                 kept[0] = x.x, kept[1] = x.y, kept[2] = x.z, kept[3] = x.w;
@@ -231,7 +246,13 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, Key
             for (int j = 0; j < 8; ++j) {
                 const int i = 8 * h + j;
                 const float p = probability<T>(s[i], a.scale, c, lse[j]);
-                if (kDrop) {
+                if (kExact) {
+                    const float seen_p = seen ? p : 0.f;
+                    const bool keep = !kDrop || (kept[j] & (1u << (lane & 31)));
+                    p8[j] = keep ? seen_p : 0.f;
+                    const float d = keep ? dp[i] : 0.f;
+                    s8[j] = seen_p * (d - sum_half(seen_p * d));
+                } else if (kDrop) {
                     const bool keep = kept[j] & (1u << (lane & 31));
                     p8[j] = keep ? p : 0.f;
                     s8[j] = p * (keep ? dp[i] : none[j]);
@@ -291,18 +312,17 @@ struct QueryTiles {
 };
 
 // The waves share tiles of keys, or with kSplitKeys (few query rows) take them in turn, as in
-// the forward.  kDelta: delta to out.delta in place of the gradient (one split).
-template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kDelta>
-__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, uint32_t item, int splits, char *lds) {
+// the forward.  kExact: the structure has kExactStates keys at most, one tile, and delta is its sum of p dp.
+template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kExact>
+__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, const Place &w, char *lds) {
     using C = QueryTiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const Place w = place_of<C::kRows>(a, item, true, splits, out.q_slots);
-    if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int thread = kSplitKeys ? lane : threadIdx.x;
     T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
 
-    const int n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
+    static_assert(kKeys >= kExactStates, "one tile");
+    const int splits = out.q_splits, n_tiles = (w.keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
     const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
     const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
@@ -327,11 +347,10 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
             const bool use = row_ok && d < a.dim && t < t_end;  // a wave without keys needs no rows
             qf[s] = use ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
             gf[s] = use ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
-            if (!kDelta && !out.delta && use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
+            if (!kExact && use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
         }
     }
-    const float none = kDelta ? 0.f : out.delta ? out.delta[at] : sum_halves(delta) * (-1.f / a.keep_scale);
-    float exact = 0.f;
+    float none = sum_halves(delta) * (-1.f / a.keep_scale);  // what dp - delta is where p was dropped
     const float lse = kept_lse<T>(row_ok ? a.lse[at] : -INFINITY);
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
@@ -346,7 +365,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
         in.fetch(a, k_base, v_base, mask, w.keys, min(t + t_step, t_end - 1));
         f32x16 s = {}, dp;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = none;
+        for (int i = 0; i < 16; ++i) dp[i] = none;  // kExact: zero
         const int row = permuted_row(lane & 31);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
@@ -357,48 +376,44 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
             each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
         }
         vec8<T> sf[2], sl[2];
+        uint32_t keep[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2 && kDrop; ++h)
+            keep[h] = keep_bits(g, (k0 + 16 * h) / 8 + half, static_cast<uint32_t>(at), a.threshold);
+        if (kExact) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (kDrop) dp[i] = keep[i >> 3] & (1u << (i & 7)) ? dp[i] : 0.f;
+                sum = fmaf(probability<T>(s[i], a.scale, c, lse), dp[i], sum);
+            }
+            none = -sum_halves(sum);
+            dp += none;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x8 s8;
-            const uint32_t keep = kDrop ? keep_bits(g, (k0 + 16 * h) / 8 + half, static_cast<uint32_t>(at), a.threshold) : 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float p = probability<T>(s[8 * h + j], a.scale, c, lse);
-                s8[j] = p * (!kDrop || (keep & (1u << j)) ? dp[8 * h + j] : none);
-                if (kDelta) exact -= s8[j];
+                s8[j] = p * (kExact || !kDrop || (keep[h] & (1u << j)) ? dp[8 * h + j] : none);
             }
             sf[h] = from_f32<T>(s8);
             if (kRest<T>) sl[h] = from_f32<T>(s8 - to_f32<T>(sf[h]));
         }
-        if constexpr (!kDelta) {
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) {
+        for (int d = 0; d < kOut; ++d) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
-                    gq[d] = mma(gq[d], k, sf[h]);
-                    if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
-                }
+            for (int h = 0; h < 2; ++h) {
+                const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
+                gq[d] = mma(gq[d], k, sf[h]);
+                if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
             }
         }
         if (!kSplitKeys) {
             k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
             v_tile = k_tile + C::kTile;
         }
-    }
-    if constexpr (kDelta) {
-        exact = sum_halves(exact);
-        if (!kSplitKeys) {
-            if (row_ok && half == 0) out.delta[at] = exact;
-            return;
-        }
-        __syncthreads();
-        float *sums = reinterpret_cast<float *>(lds);
-        if (half == 0) sums[wave * 32 + lane] = exact;
-        __syncthreads();
-        if (wave == 0 && half == 0 && row_ok)
-            out.delta[at] = sums[lane] + sums[32 + lane] + sums[64 + lane] + sums[96 + lane];
-        return;
     }
     const bool split = splits > 1;
     const int64_t part = split ? int64_t(w.split) * a.q_rows * a.heads : 0;
@@ -453,16 +468,23 @@ template <class T, int kDim, bool kDrop, bool kSplitKeys>
 __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 : 1) k_backward(AttnArgs a, Bwd out) {
     constexpr int kKeyBytes = int(sizeof(KeyLds<T, kDim>)), kQueryBytes = QueryTiles<T, kDim, kSplitKeys>::kBytes;
     __shared__ __attribute__((aligned(16))) char lds[kKeyBytes > kQueryBytes ? kKeyBytes : kQueryBytes];
-    if (blockIdx.x < out.key_blocks)
-        grad_keys<T, kDim, kDrop>(a, out, *reinterpret_cast<KeyLds<T, kDim> *>(lds));
-    else
-        grad_queries<T, kDim, kDrop, kSplitKeys, false>(a, out, blockIdx.x - static_cast<uint32_t>(out.key_blocks), out.q_splits, lds);
-}
-
-template <class T, int kDim, bool kDrop, bool kSplitKeys>
-__global__ void __launch_bounds__(kThreads, 2) k_delta(AttnArgs a, Bwd out) {
-    __shared__ __attribute__((aligned(16))) char lds[QueryTiles<T, kDim, kSplitKeys>::kLds];
-    grad_queries<T, kDim, kDrop, kSplitKeys, true>(a, out, blockIdx.x, 1, lds);
+    if (blockIdx.x < out.key_blocks) {
+        const Place w = place_of<kKeyTile>(a, blockIdx.x, false, out.k_splits, out.k_slots);
+        if (!w.any) return;
+        KeyLds<T, kDim> &tiles = *reinterpret_cast<KeyLds<T, kDim> *>(lds);
+        if constexpr (kExactDelta<T>) {
+            if (w.keys <= kExactStates) return grad_keys<T, kDim, kDrop, true>(a, out, w, tiles);
+        }
+        grad_keys<T, kDim, kDrop, false>(a, out, w, tiles);
+    } else {
+        const uint32_t item = blockIdx.x - static_cast<uint32_t>(out.key_blocks);
+        const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows>(a, item, true, out.q_splits, out.q_slots);
+        if (!w.any) return;
+        if constexpr (kExactDelta<T>) {
+            if (w.keys <= kExactStates) return grad_queries<T, kDim, kDrop, kSplitKeys, true>(a, out, w, lds);
+        }
+        grad_queries<T, kDim, kDrop, kSplitKeys, false>(a, out, w, lds);
+    }
 }
 
 // out = sum of `splits` fp32 arrays of `rows` rows of `row` values (a multiple of eight), in order, for
@@ -500,7 +522,7 @@ struct Choice {
     bool split_keys;
     int q_splits, k_splits;
     int64_t q_slots, k_slots;
-    size_t delta, part_q, part_k, bytes;  // bytes of delta and of the partial sums; k for each of k and v
+    size_t part_q, part_k, bytes;  // bytes of the partial sums; k for each of k and v
 };
 
 // Splits of a walk of `walk` rows, so that none is longer than `share`, what a workgroup has if the
@@ -511,7 +533,7 @@ int splits_of(int64_t walk, int64_t share) {
     return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-Choice choose(oeq_dtype dtype, const AttnArgs &a) {
+Choice choose(const AttnArgs &a) {
     Choice c{};
     // Twice the workgroups the chip holds at once: walks half as long even out better than their
     // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 107 us,
@@ -526,21 +548,13 @@ Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     c.k_splits = splits_of(rows, share);
     c.part_q = c.q_splits > 1 ? up(static_cast<size_t>(c.q_splits) * a.q_rows * a.heads * a.dim * 4) : 0;
     c.part_k = c.k_splits > 1 ? up(static_cast<size_t>(c.k_splits) * a.k_rows * a.kv_heads * a.dim * 4) : 0;
-    c.delta = dtype != OEQ_F32 && keys <= kExactStates ? up(static_cast<size_t>(a.q_rows) * a.heads * sizeof(float)) : 0;
-    c.bytes = c.delta + c.part_q + 2 * c.part_k;
+    c.bytes = c.part_q + 2 * c.part_k;
     return c;
 }
 
 template <class T, int kDim, bool kDrop>
 void launch(const AttnArgs &a, const Choice &c, const Bwd &out, int64_t blocks, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);
-    if constexpr (sizeof(T) == 2) {
-        const dim3 rows(static_cast<unsigned>(c.q_slots * a.kv_heads));
-        if (out.delta && c.split_keys)
-            k_delta<T, kDim, kDrop, true><<<rows, threads, 0, stream>>>(a, out);
-        else if (out.delta)
-            k_delta<T, kDim, kDrop, false><<<rows, threads, 0, stream>>>(a, out);
-    }
     if (c.split_keys)
         k_backward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, out);
     else
@@ -556,12 +570,10 @@ void launch(const AttnArgs &a, const Choice &c, const Bwd &out, int64_t blocks, 
 }
 
 template <class T>
-hipError_t backward(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
-    const Choice c = choose(dtype, a);
+hipError_t backward(const AttnArgs &a, hipStream_t stream) {
+    const Choice c = choose(a);
     char *ws = static_cast<char *>(a.workspace);
     Bwd out{};
-    if (c.delta) out.delta = reinterpret_cast<float *>(ws);
-    ws += c.delta;
     out.part_q = reinterpret_cast<float *>(ws);
     out.part_k = reinterpret_cast<float *>(ws + c.part_q);
     out.part_v = reinterpret_cast<float *>(ws + c.part_q + c.part_k);
@@ -591,18 +603,18 @@ hipError_t backward(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-size_t cross_attn_bwd_workspace(oeq_dtype dtype, const AttnArgs &a) { return choose(dtype, a).bytes; }
+size_t cross_attn_bwd_workspace(oeq_dtype, const AttnArgs &a) { return choose(a).bytes; }
 
-int64_t cross_attn_bwd_blocks(oeq_dtype dtype, const AttnArgs &a) {
-    const Choice c = choose(dtype, a);
+int64_t cross_attn_bwd_blocks(oeq_dtype, const AttnArgs &a) {
+    const Choice c = choose(a);
     return c.q_slots * a.kv_heads * c.q_splits + c.k_slots * a.kv_heads * c.k_splits;
 }
 
 hipError_t cross_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
     switch (dtype) {
-        case OEQ_F32: return backward<float>(dtype, a, stream);
-        case OEQ_F16: return backward<f16>(dtype, a, stream);
-        case OEQ_BF16: return backward<bf16>(dtype, a, stream);
+        case OEQ_F32: return backward<float>(a, stream);
+        case OEQ_F16: return backward<f16>(a, stream);
+        case OEQ_BF16: return backward<bf16>(a, stream);
         default: return hipErrorInvalidValue;
     }
 }

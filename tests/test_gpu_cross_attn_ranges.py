@@ -58,6 +58,29 @@ def both(q, k, v, g, q_len, k_len, p=0.0, key=None, mask=None):
                                    None if mask is None else host(mask), p, key, host(g))
 
 
+# ---- structures of few states beside long ones ------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("mates", [[], [2000], [9, 1, 300]])
+@pytest.mark.parametrize("rows,p", [(8, 0.0), (100, 0.0), (40, 0.25)])
+def test_gradients_of_few_states_do_not_depend_on_the_batch(rows, p, mates, kind):
+    # With few states the rounding of the saved out is most of what delta = grad_out out loses, so
+    # delta is summed from p dp there: grad_q and grad_k then only carry their own rounding
+    k_len = [2, 4, 7, 31, 32, *mates]
+    q_len = [rows] * len(k_len)
+    q, k, v, g = operands(kind, q_len, k_len, 4, 2, 32, 29)
+    mask = torch.ones(sum(k_len), dtype=torch.uint8, device="cuda")
+    mask[[9, 20, 21]] = 0  # of the third and the fourth structure
+    got, ref = both(q, k, v, g, q_len, k_len, p, (11, 12) if p else None, mask)
+    qp, kp = ptr(q_len), ptr(k_len)
+    for s in range(5):
+        for n, rows_of in (("grad_q", slice(qp[s], qp[s + 1])), ("grad_k", slice(kp[s], kp[s + 1]))):
+            want = ref[n][rows_of]
+            own = rel_l2(rounded(want, kind), want)
+            e = rel_l2(host(got[n])[rows_of], want)
+            assert e <= 1.35 * own + RTOL["f32"], (n, k_len[s], e, own)
+
+
 # ---- rows of no structure -----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", list(TYPES))
