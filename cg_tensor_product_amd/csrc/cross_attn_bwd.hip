@@ -48,6 +48,68 @@ constexpr bool kExactDelta = sizeof(T) == 2;
 template <class T>
 constexpr bool kRest = sizeof(T) == 2;
 
+// fp16 ends at 2^-24 and 65504, and score gradients, about grad_out / states, leave that range at both
+// ends.  So they are brought into it by a power of two, chosen ahead of a walk: |grad_out| (|v| + |out|),
+// of rows at hand, bounds |dp - delta| within a small factor if the other rows are alike, and p |dp - delta|
+// is put where that bound is 2^14; what p = 2^-17 leaves of it still lies 2^22 above the last bit.
+//   grad_queries  a power for each row, which is a lane and a column of its sums; p carries it;
+//   grad_keys     one for the workgroup: p carries 2^kProbBits (of it grad_v too: probabilities near
+//                 2^-16 would keep eight bits, and keep all), the rows of grad_out in LDS the rest.
+// Where a walk meets rows so much larger that a score gradient passes 65504, its sums are no longer
+// finite, and it is done again: that of queries 2^24 lower for the rows concerned, up to kTries times (enough
+// for any fp16 inputs), that of keys with care (kCare): a power for each key, from 2^60 on, falls
+// with the tile whose largest reaches 2 so that this one gets 2^-6 .. 2^-5, and the sums are scaled along;
+// what is lost is below 2^-19 of the column's largest.  With care from the start large calls take
+// 10 % longer (D = 64: each tile waits for the check).
+template <class T>
+constexpr bool kScaled = std::is_same<T, f16>::value;
+constexpr int kTries = 5, kLower = 24, kCareBits = 60;
+template <class T, bool kCare>
+constexpr int kProbBits = kScaled<T> ? (kCare ? 15 : 6) : 0;
+
+__device__ __forceinline__ float power(int bits) { return __builtin_ldexpf(1.f, bits); }
+
+// The power that puts a bound, given its square (0: not known), between 2^(to - 1) and 2^to.
+__device__ __forceinline__ int bits_ahead(int to, float bound2) {
+    return bound2 > 0.f ? to - ((__builtin_amdgcn_frexp_expf(bound2) + 1) >> 1) : 0;
+}
+
+// Whether all sums are finite (they are far from where their own sum would not be).
+template <int kOut>
+__device__ __forceinline__ bool finite(const f32x16 (&sum)[kOut]) {
+    f32x16 all = sum[0];
+#pragma unroll
+    for (int d = 1; d < kOut; ++d) all += sum[d];
+#pragma unroll
+    for (int n = 8; n > 0; n >>= 1) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) all[i] += all[n + i];
+    }
+    return fabsf(all[0]) < INFINITY;
+}
+__device__ __forceinline__ float largest(f32x16 v) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+    return max_halves(m);
+}
+// Whether a value reaches 2: below it bit 14 of fp16 is clear.
+__device__ __forceinline__ bool reaches_two(const vec8<f16> (&v)[2]) {
+    using Words = uint32_t __attribute__((ext_vector_type(4)));
+    const Words a = __builtin_bit_cast(Words, v[0]), b = __builtin_bit_cast(Words, v[1]);
+    return ((a[0] | a[1] | a[2] | a[3] | b[0] | b[1] | b[2] | b[3]) & 0x40004000u) != 0;
+}
+
+// The largest `v` of the workgroup's waves, which all of them have then brought.  Calls of one kCall have
+// another barrier between them.
+template <int kCall>
+__device__ __forceinline__ int max_wave(int v) {
+    __shared__ int of_wave[kWaves];
+    if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return max(max(of_wave[0], of_wave[1]), max(of_wave[2], of_wave[3]));
+}
+
 struct Bwd {
     float *part_q;           // [split][query row, head][dim]
     float *part_k, *part_v;  // [split][key, key head][dim]
@@ -56,9 +118,9 @@ struct Bwd {
     int64_t key_blocks;  // workgroups that own keys; the rest own query rows
 };
 
-// p from a score; fp32 forms scale s - lse in one rounding, since the difference is small
-// against its parts.  `lse` is in powers of two for 16-bit types, and +infinity for a row that
-// saw nothing, whose probabilities are zero.
+// p from a score, times 2^bits where `lse` is less by that; fp32 forms scale s - lse in one
+// rounding, since the difference is small against its parts.  `lse` is in powers of two for 16-bit
+// types, and +infinity for a row that saw nothing, whose probabilities are zero.
 template <class T>
 __device__ __forceinline__ float probability(float s, float scale, float c, float lse) {
     if (sizeof(T) == 4) return __builtin_amdgcn_exp2f(fmaf(s, scale, -lse) * kLog2E);
@@ -76,6 +138,28 @@ __device__ __forceinline__ float dot(vec8<T> a, vec8<T> b) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v = fmaf(x[j], y[j], v);
     return v;
+}
+
+// Score gradients as operands of a product: the rounded values and the rest.
+template <class T>
+__device__ __forceinline__ void two_terms(f32x8 v, vec8<T> *value, vec8<T> *rest) {
+    *value = from_f32<T>(v);
+    if (kRest<T>) *rest = from_f32<T>(v - to_f32<T>(*value));
+}
+
+// The step with care: lowers the power where a lane's score gradients `ds` reach 1 with it, scales the sums
+// and forms the terms again.  Returns by how much.
+template <class T, int kOut>
+__device__ __forceinline__ int lower(f32x16 ds, bool used, f32x16 (&sum)[kOut], vec8<T> (&value)[2], vec8<T> (&rest)[2]) {
+    const float most = largest(ds);
+    const int by = used && most >= 1.f ? -5 - __builtin_amdgcn_frexp_expf(most) : 0;
+    const float factor = power(by);
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) sum[d] *= factor;
+    ds *= factor;
+    two_terms<T>(__builtin_shufflevector(ds, ds, 0, 1, 2, 3, 4, 5, 6, 7), &value[0], &rest[0]);
+    two_terms<T>(__builtin_shufflevector(ds, ds, 8, 9, 10, 11, 12, 13, 14, 15), &value[1], &rest[1]);
+    return by;
 }
 
 // Four consecutive columns of a gradient, to the fp32 partial sums or the result.
@@ -116,18 +200,19 @@ __device__ __forceinline__ float sum_half(float v) {
 }
 
 // kExact: the structure has kExactStates keys at most, all of them in the first wave, which forms delta
-// from p dp; the other waves only bring rows.
-template <class T, int kDim, bool kDrop, bool kExact>
-__device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, const Place &w, KeyLds<T, kDim> &lds) {
+// from p dp; the other waves only bring rows.  kCare: see kScaled.  Returns false, without results, where the
+// walk is to be done again with care.  `tid` is threadIdx.x.
+template <class T, int kDim, bool kDrop, bool kExact, bool kCare>
+__device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, const Place &w, int tid, KeyLds<T, kDim> &lds) {
     constexpr int kRow = KeyLds<T, kDim>::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+    const int lane = tid & 63, half = lane >> 5, wave = tid >> 6;
     const int key = w.first + wave * 32 + (lane & 31);
     const bool key_ok = key < w.keys;
     const int64_t k_row = w.k_begin + (key_ok ? key : 0);
     const bool seen = key_ok && (!a.key_mask || a.key_mask[k_row]);
 
     using Stage = RowStage<T, kRowTile, kDim, kThreads>;
-    Stage q_in(threadIdx.x, a.dim), g_in(threadIdx.x, a.dim), o_in(threadIdx.x, a.dim);
+    Stage q_in(tid, a.dim), g_in(tid, a.dim), o_in(tid, a.dim);
     float lse_in = 0.f;
     const int n_tiles = (w.rows + kRowTile - 1) / kRowTile, per = (n_tiles + out.k_splits - 1) / out.k_splits;
     const int t_end = min(n_tiles, (w.split + 1) * per);
@@ -155,9 +240,9 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
                 if (!kExact) o_in.v[i] = *reinterpret_cast<const vec8<T> *>(static_cast<const T *>(a.out) + at[i]);
             }
         }
-        if (threadIdx.x < kRowTile) {
+        if (tid < kRowTile) {
             int64_t q_row;
-            const int r = t * kRowTile + threadIdx.x, head = row_of(r, &q_row);
+            const int r = t * kRowTile + tid, head = row_of(r, &q_row);
             lse_in = a.lse[q_row * a.heads + head];
         }
     };
@@ -180,6 +265,26 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
     if (kDrop) g = load_rng(a.rng);
     const float c = a.scale * kLog2E, start = -1.f / a.keep_scale;
     f32x16 gk[kOut] = {}, gv[kOut] = {};
+    constexpr int kProb = kProbBits<T, kCare>;
+    int bits = kScaled<T> && kCare ? kCareBits - kProb : 0;  // with kProb the power of gk; not kCare: of grad_out
+    if constexpr (kScaled<T> && !kCare) {
+        // the rows that this wave brings for the first tile stand for all
+        float gg = 0.f, oo = 0.f, vv = 0.f;
+        if (t < t_end && q_in.reads) {
+#pragma unroll
+            for (int i = 0; i < Stage::kPieces; ++i) {
+                gg += dot<T>(g_in.v[i], g_in.v[i]);
+                oo += dot<T>(o_in.v[i], o_in.v[i]);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) vv += dot<T>(vf[s], vf[s]);
+        // of its keys together, and of the waves the one with the largest bound
+        const float bound2 = sum_halves(sum_half(gg)) * sum_halves(sum_half(vv + oo));
+        bits = -max_wave<0>(__builtin_amdgcn_readfirstlane(-bits_ahead(14 - kProb, bound2)));
+        bits = max(min(bits, 15), -24);  // what one factor of fp16 can be
+    }
+    float up = power(bits);
 
     for (int buffer = 0; t < t_end; ++t, buffer ^= 1) {
         const int r0 = t * kRowTile, in_tile = min(kRowTile, w.rows - r0);
@@ -188,6 +293,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
 #pragma unroll
             for (int i = 0; i < Stage::kPieces; ++i) {
                 const int row = q_in.row + i * Stage::kStep;
+                if (kScaled<T> && !kCare) g_in.v[i] *= static_cast<T>(up);
                 float v = q_in.reads ? dot<T>(g_in.v[i], o_in.v[i]) : 0.f;
 #pragma unroll
                 for (int off = 1; off < Stage::kLanes; off <<= 1) v += __shfl_xor(v, off);
@@ -198,7 +304,10 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
         // zero, and NaN only where the last row's are (zeros would give NaN against an infinite state).
         q_in.store(q_tile, true, 0);
         g_in.store(g_tile, true, 0);
-        if (threadIdx.x < kRowTile) lds.lse[buffer][threadIdx.x] = static_cast<int>(threadIdx.x) < in_tile ? kept_lse<T>(lse_in) : INFINITY;
+        if (tid < kRowTile) {
+            const float lse = kept_lse<T>(lse_in) - float(kProb);
+            lds.lse[buffer][tid] = tid < in_tile ? lse : INFINITY;
+        }
         if (kDrop) {
             // 32 rows x 4 generator blocks of this wave's keys, two a lane; a row's bits make a word
             wave_sync();
@@ -251,7 +360,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
                     const bool keep = !kDrop || (kept[j] & (1u << (lane & 31)));
                     p8[j] = keep ? seen_p : 0.f;
                     const float d = keep ? dp[i] : 0.f;
-                    s8[j] = seen_p * (d - sum_half(seen_p * d));
+                    s8[j] = seen_p * (d - sum_half(seen_p * d) * (1.f / (1 << kProb)));
                 } else if (kDrop) {
                     const bool keep = kept[j] & (1u << (lane & 31));
                     p8[j] = keep ? p : 0.f;
@@ -262,8 +371,19 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
                 }
             }
             pf[h] = from_f32<T>(p8);
-            sf[h] = from_f32<T>(s8);
-            if (kRest<T>) sl[h] = from_f32<T>(s8 - to_f32<T>(sf[h]));
+            if (kScaled<T> && kCare) {
+                s8 *= up;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dp[8 * h + j] = s8[j];
+            }
+            two_terms<T>(s8, &sf[h], &sl[h]);
+        }
+        if constexpr (kScaled<T> && kCare) {
+            if (__any(seen && reaches_two(sf))) {
+                rare();
+                bits += lower<T>(dp, seen, gk, sf, sl);
+                up = power(bits);
+            }
         }
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
@@ -276,10 +396,14 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
             }
         }
     }
-    if (!key_ok) return;
+    if constexpr (kScaled<T> && !kCare) {
+        if (max_wave<1>(__any(seen && !finite(gk)))) return false;
+    }
+    if (!key_ok) return true;
     const bool split = out.k_splits > 1;
     const int64_t at = (split ? int64_t(w.split) * a.k_rows * a.kv_heads : 0) + k_row * a.kv_heads + w.kv_head;
-    const float k_factor = a.scale * a.keep_scale, v_factor = a.keep_scale;
+    const float k_factor = a.scale * a.keep_scale * power(-bits - kProb);
+    const float v_factor = a.keep_scale * power(kScaled<T> && !kCare ? -bits - kProb : -kProb);
 #pragma unroll
     for (int d = 0; d < kOut; ++d) {
 #pragma unroll
@@ -296,6 +420,7 @@ __device__ __forceinline__ void grad_keys(const AttnArgs &a, const Bwd &out, con
             }
         }
     }
+    return true;
 }
 
 template <class T, int kDim, bool kSplitKeys>
@@ -328,8 +453,8 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
     const uint8_t *mask = a.key_mask ? a.key_mask + w.k_begin : nullptr;
     KeyStage<T, kKeys, kDim, C::kStage> in(thread, a.dim);
-    int t = w.split * per + (kSplitKeys ? wave : 0);
-    if (t < t_end) in.fetch(a, k_base, v_base, mask, w.keys, t);
+    const int t_begin = w.split * per + (kSplitKeys ? wave : 0);
+    if (t_begin < t_end) in.fetch(a, k_base, v_base, mask, w.keys, t_begin);
 
     const int r = w.first + (kSplitKeys ? 0 : wave * 32) + (lane & 31);
     const bool row_ok = r < w.rows;
@@ -337,17 +462,21 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     const int head = w.kv_head * a.share + (row_ok ? r % a.share : 0);
     const int64_t at = q_row * a.heads + head;
     vec8<T> qf[kSteps], gf[kSteps];
-    float delta = 0.f;
+    float delta = 0.f, gg = 0.f, oo = 0.f;  // of grad_out and out: their product and squares
     {
         const T *q = static_cast<const T *>(a.q) + q_row * a.q_row + head * a.q_head;
         const T *g = static_cast<const T *>(a.grad_out) + at * a.dim, *o = static_cast<const T *>(a.out) + at * a.dim;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int d = 16 * s + 8 * half;
-            const bool use = row_ok && d < a.dim && t < t_end;  // a wave without keys needs no rows
+            const bool use = row_ok && d < a.dim && t_begin < t_end;  // a wave without keys needs no rows
             qf[s] = use ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
             gf[s] = use ? *reinterpret_cast<const vec8<T> *>(g + d) : vec8<T>(T(0.f));
-            if (!kExact && use) delta += dot<T>(gf[s], *reinterpret_cast<const vec8<T> *>(o + d));
+            if (!kExact && use) {
+                const vec8<T> of = *reinterpret_cast<const vec8<T> *>(o + d);
+                delta += dot<T>(gf[s], of);
+                if (kScaled<T>) gg += dot<T>(gf[s], gf[s]), oo += dot<T>(of, of);
+            }
         }
     }
     float none = sum_halves(delta) * (-1.f / a.keep_scale);  // what dp - delta is where p was dropped
@@ -355,65 +484,87 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     Rng g{};
     if (kDrop) g = load_rng(a.rng);
     const float c = a.scale * kLog2E;
-    f32x16 gq[kOut] = {};
+    f32x16 gq[kOut];
+    int bits = kScaled<T> && !kExact ? bits_ahead(14, sum_halves(gg) * sum_halves(oo)) : 0;  // the power of gq
 
-    for (int buffer = 0; t < t_end; t += t_step) {
-        if (kSplitKeys) wave_sync();
-        const uint64_t valid = in.store(k_tile, v_tile);
-        if (kSplitKeys) wave_sync(); else __syncthreads();
-        const int k0 = t * kKeys;
-        in.fetch(a, k_base, v_base, mask, w.keys, min(t + t_step, t_end - 1));
-        f32x16 s = {}, dp;
+    for (int tries = 1;; ++tries) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = none;  // kExact: zero
-        const int row = permuted_row(lane & 31);
+        for (int d = 0; d < kOut; ++d) gq[d] = f32x16{};
+        const float p_lse = lse - (kScaled<T> ? float(bits) : 0.f);
+        for (int t = t_begin, buffer = 0; t < t_end; t += t_step) {
+            if (kSplitKeys) wave_sync();
+            const uint64_t valid = in.store(k_tile, v_tile);
+            if (kSplitKeys) wave_sync(); else __syncthreads();
+            const int k0 = t * kKeys;
+            in.fetch(a, k_base, v_base, mask, w.keys, min(t + t_step, t_end - 1));
+            f32x16 s = {}, dp;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
+            for (int i = 0; i < 16; ++i) dp[i] = none;  // kExact: zero
+            const int row = permuted_row(lane & 31);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(v_tile, kRow, row, 16 * i, half), gf[i]);
-        if (valid != ~0ull) {
-            rare();
-            each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
-        }
-        vec8<T> sf[2], sl[2];
-        uint32_t keep[2] = {};
+            for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
 #pragma unroll
-        for (int h = 0; h < 2 && kDrop; ++h)
-            keep[h] = keep_bits(g, (k0 + 16 * h) / 8 + half, static_cast<uint32_t>(at), a.threshold);
-        if (kExact) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (kDrop) dp[i] = keep[i >> 3] & (1u << (i & 7)) ? dp[i] : 0.f;
-                sum = fmaf(probability<T>(s[i], a.scale, c, lse), dp[i], sum);
+            for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(v_tile, kRow, row, 16 * i, half), gf[i]);
+            if (valid != ~0ull) {
+                rare();
+                each_score(static_cast<uint32_t>(valid), half, [&](int i, bool used) { s[i] = used ? s[i] : -INFINITY; });
             }
-            none = -sum_halves(sum);
-            dp += none;
-        }
+            vec8<T> sf[2], sl[2];
+            uint32_t keep[2] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f32x8 s8;
+            for (int h = 0; h < 2 && kDrop; ++h)
+                keep[h] = keep_bits(g, (k0 + 16 * h) / 8 + half, static_cast<uint32_t>(at), a.threshold);
+            if (kExact) {
+                float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p = probability<T>(s[8 * h + j], a.scale, c, lse);
-                s8[j] = p * (kExact || !kDrop || (keep[h] & (1u << j)) ? dp[8 * h + j] : none);
+                for (int i = 0; i < 16; ++i) {
+                    if (kDrop) dp[i] = keep[i >> 3] & (1u << (i & 7)) ? dp[i] : 0.f;
+                    sum = fmaf(probability<T>(s[i], a.scale, c, lse), dp[i], sum);
+                }
+                none = -sum_halves(sum);
+                dp += none;
+                if (kScaled<T>) {  // the one tile's own power
+                    f32x16 ds;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ds[i] = probability<T>(s[i], a.scale, c, lse) * dp[i];
+                    const float most = largest(ds);
+                    bits = most > 0.f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
+                    dp *= power(bits);
+                }
             }
-            sf[h] = from_f32<T>(s8);
-            if (kRest<T>) sl[h] = from_f32<T>(s8 - to_f32<T>(sf[h]));
-        }
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
-                gq[d] = mma(gq[d], k, sf[h]);
-                if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
+                f32x8 s8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = probability<T>(s[8 * h + j], a.scale, c, kExact ? lse : p_lse);
+                    s8[j] = p * (kExact || !kDrop || (keep[h] & (1u << j)) ? dp[8 * h + j] : none);
+                }
+                two_terms<T>(s8, &sf[h], &sl[h]);
+            }
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
+                    gq[d] = mma(gq[d], k, sf[h]);
+                    if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
+                }
+            }
+            if (!kSplitKeys) {
+                k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
+                v_tile = k_tile + C::kTile;
             }
         }
-        if (!kSplitKeys) {
-            k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
-            v_tile = k_tile + C::kTile;
-        }
+        if constexpr (!kScaled<T> || kExact) break;
+        const bool again = !finite(gq), any = __any(again);
+        if (!(kSplitKeys ? any : max_wave<2>(any)) || tries == kTries) break;
+        if (again) bits -= kLower;
+        in.fetch(a, k_base, v_base, mask, w.keys, t_begin);
+    }
+    if (kScaled<T>) {
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) gq[d] *= power(-bits);
     }
     const bool split = splits > 1;
     const int64_t part = split ? int64_t(w.split) * a.q_rows * a.heads : 0;
@@ -461,23 +612,33 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     }
 }
 
-// Two workgroups a compute unit, where that does not leave too few registers: against one, D = 96
+// Three workgroups a compute unit at D = 32 (fp16 with dropout, 64 structures of up to 32 rows and 200
+// states: 21.5 us for 25.0 with two), else two, where that does not leave too few registers: against one, D = 96
 // takes 165 us for 279 and D = 128 239 for 328 (bf16, 4 structures of 1024 query rows and 2048
 // states, 8 heads over 4); fp32 at D = 128 would take 1369 for 1102.
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
-__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 || kDim <= 64) ? 2 : 1) k_backward(AttnArgs a, Bwd out) {
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 && kDim <= 32) ? 3 : (sizeof(T) == 2 || kDim <= 64) ? 2 : 1)
+    k_backward(AttnArgs a, Bwd out) {
     constexpr int kKeyBytes = int(sizeof(KeyLds<T, kDim>)), kQueryBytes = QueryTiles<T, kDim, kSplitKeys>::kBytes;
     __shared__ __attribute__((aligned(16))) char lds[kKeyBytes > kQueryBytes ? kKeyBytes : kQueryBytes];
-    if (blockIdx.x < out.key_blocks) {
-        const Place w = place_of<kKeyTile>(a, blockIdx.x, false, out.k_splits, out.k_slots);
-        if (!w.any) return;
+    uint32_t block = blockIdx.x;
+    if (block < out.key_blocks) {
         KeyLds<T, kDim> &tiles = *reinterpret_cast<KeyLds<T, kDim> *>(lds);
-        if constexpr (kExactDelta<T>) {
-            if (w.keys <= kExactStates) return grad_keys<T, kDim, kDrop, true>(a, out, w, tiles);
+        int tid = threadIdx.x;
+        const auto place = [&]() { return place_of<kKeyTile>(a, block, false, out.k_splits, out.k_slots); };
+        const Place w = place();
+        if (!w.any) return;
+        if (kExactDelta<T> && w.keys <= kExactStates) {
+            grad_keys<T, kDim, kDrop, kExactDelta<T>, kScaled<T>>(a, out, w, tid, tiles);
+        } else if (!grad_keys<T, kDim, kDrop, false, false>(a, out, w, tid, tiles)) {
+            if constexpr (kScaled<T>) {
+                // finds its place and its thread anew: kept for this, they would take registers of the other walk
+                asm volatile("" : "+s"(block), "+v"(tid));
+                grad_keys<T, kDim, kDrop, false, true>(a, out, place(), tid, tiles);
+            }
         }
-        grad_keys<T, kDim, kDrop, false>(a, out, w, tiles);
     } else {
-        const uint32_t item = blockIdx.x - static_cast<uint32_t>(out.key_blocks);
+        const uint32_t item = block - static_cast<uint32_t>(out.key_blocks);
         const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows>(a, item, true, out.q_splits, out.q_slots);
         if (!w.any) return;
         if constexpr (kExactDelta<T>) {

@@ -58,6 +58,116 @@ def both(q, k, v, g, q_len, k_len, p=0.0, key=None, mask=None):
                                    None if mask is None else host(mask), p, key, host(g))
 
 
+# ---- score gradients and probabilities far from one ----------------------------------------------
+
+# Query rows, states, size of grad_out.  The score gradients of a row are about grad_out / states:
+# down to 1e-7 here, below fp16's smallest normal number (6e-5) and its last bit (6e-8).
+SMALL = [(64, 2048, 1e-2), (64, 2048, 1e-3), (1024, 2048, 1e-3), (20, 8192, 1e-2), (130, 8192, 1e-3)]
+
+
+@pytest.mark.parametrize("rows,states,size", SMALL)
+def test_half_gradients_of_small_score_gradients(rows, states, size):
+    # grad_q and grad_k: the result's rounding and a tenth of it from out within delta (its share is
+    # 1 / sqrt(states in use)); grad_v: the probabilities are rounded as well, sqrt(2) of it
+    q, k, v, g = operands("f16", [rows], [states], 1, 1, 64, rows + states, size)
+    got, ref = both(q, k, v, g, [rows], [states])
+    for n, times in (("grad_q", 1.35), ("grad_k", 1.35), ("grad_v", 1.75)):
+        own = rel_l2(rounded(ref[n], "f16"), ref[n])
+        e = rel_l2(host(got[n]), ref[n])
+        assert e <= times * own + RTOL["f32"], (n, e, own)
+
+
+def test_half_gradient_to_values_of_many_states():
+    # probabilities near 1e-5, where fp16's steps of 6e-8 are 0.6 % of them
+    q, k, v, g = operands("f16", [40], [100000], 1, 1, 32, 5)
+    got, ref = both(q, k, v, g, [40], [100000])
+    own = rel_l2(rounded(ref["grad_v"], "f16"), ref["grad_v"])
+    e = rel_l2(host(got["grad_v"]), ref["grad_v"])
+    assert e <= 1.75 * own + RTOL["f32"], (e, own)
+
+
+@pytest.mark.parametrize("q_len,k_len", [([40], [5]), ([100, 3], [40, 3]), ([2, 1], [90, 70])])
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_half_gradients_of_large_score_gradients(q_len, k_len, p):
+    # score gradients past 65504, the largest fp16 number, whose gradients to q and k are not.
+    # 2^-11 four times (probabilities, out within delta, the rest, the result), as everywhere
+    q, k, v, g = operands("f16", q_len, k_len, 2, 2, 64, 17, 4000.0)
+    k, q = k * 0.125, q * 0.125
+    v = v * 4
+    got, ref = both(q, k, v, g, q_len, k_len, p, (3, 4) if p else None)
+    for n in ("grad_q", "grad_k", "grad_v"):
+        assert np.abs(ref[n]).max() < 65504, n  # the exact results fit
+        assert torch.isfinite(got[n]).all(), n
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * 2.0 ** -11 + RTOL["f32"], n
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows", [3, 70])
+def test_gradients_of_score_gradients_that_grow_and_vanish(rows, kind):
+    # values, and with them the score gradients, grow by 2^20 along the states (each wave's running
+    # scale has to follow) and are exactly zero for the first hundred and the last
+    q, k, v, g = operands(kind, [rows], [700], 2, 1, 32, 23)
+    steps = torch.linspace(-12, 8, 700, device="cuda").exp2()
+    steps[:100] = 0
+    steps[-100:] = 0
+    v = (v.float() * steps[:, None, None]).to(v.dtype)
+    g[: rows // 2] = 0
+    got, ref = both(q, k, v, g, [rows], [700])
+    u = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    for n in ("grad_q", "grad_k", "grad_v"):
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
+    assert torch.all(got["grad_q"][: rows // 2] == 0)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("q_len,k_len", [([500], [70]), ([300, 9], [1000, 40]), ([40], [600])])
+@pytest.mark.parametrize("down", [False, True])
+def test_gradients_of_rows_of_very_different_size(q_len, k_len, down, kind):
+    # grad_out grows (or falls) by 2^20 along the rows, so what the first rows of a walk suggest for the
+    # others is far off
+    q, k, v, g = operands(kind, q_len, k_len, 4, 2, 64, 43)
+    steps = torch.linspace(-14, 6, q.shape[0], device="cuda").exp2()
+    g = (g.float() * (steps.flip(0) if down else steps)[:, None, None]).to(g.dtype)
+    got, ref = both(q, k, v, g, q_len, k_len)
+    u = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    for n in ("grad_q", "grad_k", "grad_v"):
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows", [3, 200])
+def test_gradients_of_values_whose_output_cancels(rows, kind):
+    # pairs of states with the same scores and opposite values (size 1000), so that the output, which tells
+    # the size of a row's values, is a small rest.  Their keys are opposite where the queries are zero,
+    # and there the two gradients of a pair add up
+    q, k, v, g = operands(kind, [rows], [80], 2, 1, 32, 59)
+    q[..., 16:] = 0
+    v *= 1000
+    k[1::2], v[1::2] = k[::2], -v[::2]
+    k[1::2, :, 16:] *= -1
+    v[0, 0, :] *= 1.0078125
+    got, ref = both(q, k, v, g, [rows], [80])
+    # delta, of an output of the rest's size, is small against the gradients: 4 u as everywhere
+    u = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    for n in ("grad_q", "grad_k", "grad_v"):
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
+
+
+def test_half_gradients_of_bad_values_stay_with_their_rows():
+    # NaN and infinite rows of grad_out reach every state of their structure and nothing else
+    q, k, v, g = operands("f16", [70, 40], [90, 50], 2, 1, 32, 53)
+    clean, _ = both(q, k, v, g, [70, 40], [90, 50])
+    for bad in (float("nan"), float("inf")):
+        h = g.clone()
+        h[5, 1, 3] = bad
+        got, _ = both(q, k, v, h, [70, 40], [90, 50])
+        assert torch.isnan(got["grad_q"][5, 1]).all()
+        assert torch.equal(got["grad_q"][:5], clean["grad_q"][:5]) and torch.equal(got["grad_q"][6:], clean["grad_q"][6:])
+        assert not torch.isfinite(got["grad_k"][:90]).any()
+        assert torch.equal(got["grad_k"][90:], clean["grad_k"][90:])
+        assert torch.equal(got["grad_v"][90:], clean["grad_v"][90:])
+
+
 # ---- structures of few states beside long ones ------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
