@@ -245,6 +245,16 @@ def _heads(t, shape, dtype, dev, name):
     return (row if shape[0] > 1 else 0), (head if shape[1] > 1 else 0)
 
 
+def _number(v, name):
+    """v as a float: what is remembered by value must not be an object that can change (a tensor)."""
+    if type(v) is float:
+        return v
+    try:
+        return v.__float__()
+    except AttributeError:
+        raise TypeError(f"{name} must be a number") from None
+
+
 @functools.lru_cache(maxsize=4096)
 def _attn_desc(*fields):
     """(descriptor, workspace bytes forward, backward), a function of sizes, strides and numbers."""
@@ -276,7 +286,8 @@ def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
     if key_mask is not None:
         mask = _dense(key_mask, (tk,), torch.bool if key_mask.dtype is torch.bool else _U8, dev, "key_mask")
     desc = _attn_desc(code, B, h, hk, d, tq, tk, *_heads(q, shape, dt, dev, "q"), *_heads(k, kv, dt, dev, "k"),
-                      *_heads(v, kv, dt, dev, "v"), d ** -0.5 if scale is None else scale, p_drop)
+                      *_heads(v, kv, dt, dev, "v"), d ** -0.5 if scale is None else _number(scale, "scale"),
+                      _number(p_drop, "p_drop"))
     return dev, desc, (q_ptr.data_ptr(), k_ptr.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), mask,
                        _dense(rng, (2,), _I64, dev, "rng"))
 

@@ -235,3 +235,23 @@ def test_gradients_of_states_with_minus_infinite_scores(q_len, k_len, kind):
     for n in ("grad_k", "grad_v"):
         assert torch.all(got[n][::2] == 0), n
         assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
+
+
+# ---- the call's own numbers ---------------------------------------------------------------------------
+
+def test_scale_and_probability_are_read_at_each_call():
+    # numbers that a program holds in tensors and changes in place between two calls
+    q, k, v, _ = operands("f32", [4], [9], 2, 1, 16, 41)
+    args = (q, k, v, index([0, 4]), index([0, 9]))
+    key = torch.tensor([1, 2], device="cuda")
+    scale, p = torch.tensor(0.25, dtype=torch.float64), torch.tensor(0.5, dtype=torch.float64)
+    for s, drop in ((0.25, 0.5), (0.75, 0.5), (0.75, 0.125)):
+        scale.fill_(s)
+        p.fill_(drop)
+        got = oeq.oeq_cross_attn_fwd(*args, scale=scale, p_drop=p, rng=key)
+        want = oeq.oeq_cross_attn_fwd(*args, scale=s, p_drop=drop, rng=key)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (s, drop)
+    got = oeq.oeq_cross_attn_fwd(*args, scale=np.float32(0.5))
+    assert torch.equal(got[0], oeq.oeq_cross_attn_fwd(*args, scale=0.5)[0])
+    with pytest.raises(TypeError):
+        oeq.oeq_cross_attn_fwd(*args, scale="0.25")
