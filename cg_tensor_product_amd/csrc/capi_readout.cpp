@@ -82,8 +82,8 @@ oeq_status check_groups(int64_t n_rows, int32_t n_struct, int32_t channels, int3
     if (channels < 1 || groups < 1 || channels % groups)
         return fail(OEQ_ERR_INVALID_ARG, "n_groups must divide n_channels");
     if (channels / groups > 2048) return fail(OEQ_ERR_UNSUPPORTED, "more than 2048 channels in a group");
-    if (n_struct > 0 && ro::group_norm_blocks(n_rows, n_struct, channels, groups) >= (int64_t(1) << 24))
-        return fail(OEQ_ERR_UNSUPPORTED, "too many structures and groups for one launch");
+    if (ro::group_norm_blocks(n_rows, n_struct, channels, groups) >= (int64_t(1) << 24))
+        return fail(OEQ_ERR_UNSUPPORTED, "too many structures, groups or channels for one launch");
     return OEQ_OK;
 }
 

@@ -591,11 +591,11 @@ __global__ void __launch_bounds__(kThreads) k_gradient_sums(GroupNormArgs a, Sha
     });
 }
 
-// The first `join_blocks` workgroups join the parts' group sums to means (one wave a
+// The first `by_group` workgroups join the parts' group sums to means (one wave a
 // (structure, group)); the others sum `column` over its rows, kJoinChannels a workgroup.
 __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Shape s, const double2 *partial,
-                                                             float2 *joined, const float *column, int join_blocks) {
-    if (static_cast<int>(blockIdx.x) < join_blocks) {
+                                                             float2 *joined, const float *column, int by_group) {
+    if (static_cast<int>(blockIdx.x) < by_group) {
         const int64_t at = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
         if (at >= int64_t(a.n_struct) * a.groups) return;
         const int b = static_cast<int>(at / a.groups), g = static_cast<int>(at % a.groups), lane = threadIdx.x & 63;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads) k_join_gradients(GroupNormArgs a, Sh
     __shared__ double part[2][kThreads];
     constexpr int kLanes = kThreads / kJoinChannels, kAhead = 8;
     const int col = threadIdx.x % kJoinChannels, lane = threadIdx.x / kJoinChannels;
-    const int c = (blockIdx.x - join_blocks) * kJoinChannels + col;
+    const int c = (blockIdx.x - by_group) * kJoinChannels + col;
     const int n_parts = static_cast<int>(s.parts);
     double u = 0, v = 0;
     if (c < a.channels) {
@@ -682,6 +682,10 @@ Pieces pieces_of(const Shape &s, int32_t n_struct, int32_t channels, int32_t gro
     return w;
 }
 
+// Workgroups of the joining kernels: one wave a (structure, group), and kJoinChannels channels.
+int64_t join_blocks(int32_t n_struct, int32_t groups) { return (int64_t(n_struct) * groups + 3) / 4; }
+int64_t channel_blocks(int32_t channels) { return (int64_t(channels) + kJoinChannels - 1) / kJoinChannels; }
+
 template <class T, bool kFull, bool kSilu>
 hipError_t forward(const GroupNormArgs &a, hipStream_t stream) {
     const Shape s = shape_of(a.rows, a.n_struct, a.channels, a.groups);
@@ -692,7 +696,7 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t stream) {
     }
     double2 *partial = static_cast<double2 *>(a.workspace);
     k_statistics<T, kFull><<<grid, threads, 0, stream>>>(a, s, partial);
-    const dim3 join(static_cast<unsigned>((int64_t(a.n_struct) * a.groups + 3) / 4));
+    const dim3 join(static_cast<unsigned>(join_blocks(a.n_struct, a.groups)));
     k_join_statistics<<<join, threads, 0, stream>>>(a, s, partial);
     k_apply<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s);
     return hipGetLastError();
@@ -701,11 +705,11 @@ hipError_t forward(const GroupNormArgs &a, hipStream_t stream) {
 template <class T, bool kFull, bool kSilu>
 hipError_t backward(const GroupNormArgs &a, hipStream_t stream) {
     const bool params = a.grad_weight || a.grad_bias;
-    const int channel_blocks = params ? (a.channels + kJoinChannels - 1) / kJoinChannels : 0;
+    const int by_channel = params ? static_cast<int>(channel_blocks(a.channels)) : 0;
     const dim3 threads(kThreads);
     if (a.rows == 0 || a.n_struct == 0) {  // no parts: zeros
         if (params)
-            k_join_gradients<<<dim3(channel_blocks), threads, 0, stream>>>(a, Shape{}, nullptr, nullptr, nullptr, 0);
+            k_join_gradients<<<dim3(by_channel), threads, 0, stream>>>(a, Shape{}, nullptr, nullptr, nullptr, 0);
         return hipGetLastError();
     }
     const Shape s = shape_of(a.rows, a.n_struct, a.channels, a.groups);
@@ -717,13 +721,12 @@ hipError_t backward(const GroupNormArgs &a, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(s.parts * s.n_slabs));
     if (!s.tile) {
         k_backward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, column);
-        if (params) k_join_gradients<<<dim3(channel_blocks), threads, 0, stream>>>(a, s, partial, joined, column, 0);
+        if (params) k_join_gradients<<<dim3(by_channel), threads, 0, stream>>>(a, s, partial, joined, column, 0);
         return hipGetLastError();
     }
     k_gradient_sums<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, column, partial);
-    const int join_blocks = a.grad_x ? static_cast<int>((int64_t(a.n_struct) * a.groups + 3) / 4) : 0;
-    k_join_gradients<<<dim3(join_blocks + channel_blocks), threads, 0, stream>>>(a, s, partial, joined, column,
-                                                                                join_blocks);
+    const int by_group = a.grad_x ? static_cast<int>(join_blocks(a.n_struct, a.groups)) : 0;
+    k_join_gradients<<<dim3(by_group + by_channel), threads, 0, stream>>>(a, s, partial, joined, column, by_group);
     if (a.grad_x) k_apply_backward<T, kFull, kSilu><<<grid, threads, 0, stream>>>(a, s, joined);
     return hipGetLastError();
 }
@@ -761,7 +764,9 @@ GroupNormBytes group_norm_workspace(int64_t rows, int32_t n_struct, int32_t chan
 
 int64_t group_norm_blocks(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups) {
     const Shape s = shape_of(rows, n_struct, channels, groups);
-    return s.parts * s.n_slabs;
+    const int64_t main = s.parts * s.n_slabs;
+    const int64_t join = (s.tile ? join_blocks(n_struct, groups) : 0) + channel_blocks(channels);
+    return main > join ? main : join;
 }
 
 hipError_t group_norm_fwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream) {

@@ -44,7 +44,7 @@ struct GroupNormArgs {
 struct GroupNormBytes {
     size_t fwd, bwd;
 };
-// Workspace bytes, and the workgroups of a launch.
+// Workspace bytes, and the workgroups of the largest launch.
 GroupNormBytes group_norm_workspace(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups);
 int64_t group_norm_blocks(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups);
 hipError_t group_norm_fwd(oeq_dtype dtype, const GroupNormArgs &a, hipStream_t stream);

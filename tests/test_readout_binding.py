@@ -1,5 +1,7 @@
 """What the readout operators' Python binding and size checks refuse before any device work (no GPU
 needed)."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -20,3 +22,14 @@ def test_a_workspace_is_a_contiguous_tensor_of_the_operands_device():
     for bad in (good[:1].expand(4096), good[::2], words.t()):  # counts more or other bytes than it owns
         with pytest.raises(ValueError):
             readout._scratch(16, bad, here)
+
+
+def test_group_norm_sizes_whose_joining_launch_is_too_large_are_refused():
+    # every launch of a call holds fewer than 2^32 threads, the joins of (structure, group) and of the
+    # channels among them: 70000 structures of 130 rows, 1024 groups
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    size = oeq.lib().oeq_group_norm_workspace_size
+    assert size(9_100_000, 70_000, 1024, 1024, ctypes.byref(f), ctypes.byref(b)) == 2
+    assert size(9_100_000, 70_000, 1024, 64, ctypes.byref(f), ctypes.byref(b)) == 0
+    # of no structures and no rows the weights' gradients are still written, 8 channels a workgroup
+    assert size(0, 0, 2**31 - 2048, (2**31 - 2048) // 2048, ctypes.byref(f), ctypes.byref(b)) == 2
