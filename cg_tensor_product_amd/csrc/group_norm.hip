@@ -270,8 +270,12 @@ struct GroupLanes {
 __device__ __forceinline__ float rstd_of(double m2, double n, float eps) {
     if (!(n > 0)) return 0.f;
     const double var = m2 > 0 || !(m2 == m2) ? m2 / n : 0;  // rounding can leave a small negative sum
-    const float v = static_cast<float>(var + double(eps)), r = __builtin_amdgcn_rsqf(v);
-    return v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;  // a Newton step; rsq(inf) is 0 already
+    // A Newton step; rsq(inf) is 0 already.  rsq takes what is below the normal numbers for zero (1e-40 is
+    // an eps too), so small values go through it times 2^64.
+    const double sum = var + double(eps);
+    const bool small = sum < 0x1p-96;
+    const float v = static_cast<float>(small ? sum * 0x1p64 : sum), r = __builtin_amdgcn_rsqf(v);
+    return v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) * (small ? 0x1p32f : 1.f) : r;
 }
 
 // Statistics of each group of the slab over the part's rows; emit(group of the slab, mean, sum
@@ -572,7 +576,7 @@ __device__ __forceinline__ void apply_backward(const GroupNormArgs &a, const Par
                                                const vec8<T> (&hx)[kStep], const vec8<T> (&hg)[kStep], f32x8 m1, f32x8 m2) {
     if (p.count <= 0) return;
     Walk<T, kFull> x(a.x, a.ld_x, p), g(a.grad_out, a.ld_grad_out, p), out(a.grad_x, a.ld_grad_x, p);
-    const f32x8 k1 = ch.rstd * m1, k2 = ch.rstd * ch.rstd * m2;
+    const f32x8 k1 = ch.rstd * m1, k2 = ch.rstd * (ch.rstd * m2);
     const auto apply = [&](const vec8<T>(&rx)[kStep], const vec8<T>(&rg)[kStep], int left) {
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {

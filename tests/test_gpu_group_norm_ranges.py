@@ -65,3 +65,20 @@ def test_group_norm_of_channels_with_means_of_their_own(rows):
     assert rel_l2(host(mean), ref["mean"]) <= RTOL["f32"]
     assert rel_l2(host(rstd), ref["rstd"]) <= RTOL["f32"]
     assert rel_l2(host(out), ref["out"]) <= RTOL["f32"]
+
+
+@pytest.mark.parametrize("rows", [1, 50, 900])
+@pytest.mark.parametrize("eps", [1e-5, 1e-30, 1.2e-38, 1e-40, 1e-44])
+def test_group_norm_of_equal_values_with_a_tiny_eps(rows, eps):
+    # no variance: rstd = 1 / sqrt(eps), finite for every fp32 eps above zero, and xhat = 0
+    x = torch.full((rows, 8), 3.5, device="cuda")
+    bias = torch.arange(8.0, device="cuda")
+    out, mean, rstd = oeq.oeq_group_norm_fwd(x, index([0, rows]), 2, None, bias, eps=eps)
+    want = 1.0 / np.sqrt(np.float64(np.float32(eps)))
+    assert np.abs(host(rstd) / want - 1).max() <= RTOL["f32"]
+    assert torch.all(mean == 3.5) and torch.equal(out, bias.expand_as(out))
+    g = torch.from_numpy(np.random.default_rng(7).normal(size=(rows, 8))).float().cuda()
+    gx, gw, gb = oeq.oeq_group_norm_bwd(x, index([0, rows]), 2, mean, rstd, g, None, bias)
+    ref = readout.group_norm(host(x), [0, rows], 2, None, host(bias), eps=np.float64(np.float32(eps)), grad_out=host(g))
+    assert rel_l2(host(gx), ref["grad_x"]) <= RTOL["f32"]
+    assert torch.all(gw == 0) and rel_l2(host(gb), ref["grad_bias"]) <= RTOL["f32"]
