@@ -279,9 +279,11 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) vv += dot<T>(vf[s], vf[s]);
-        // of its keys together, and of the waves the one with the largest bound
-        const float bound2 = sum_halves(sum_half(gg)) * sum_halves(sum_half(vv + oo));
-        bits = -max_wave<0>(__builtin_amdgcn_readfirstlane(-bits_ahead(14 - kProb, bound2)));
+        // of its keys together, and of the waves the one with the largest bound; grad_out has to fit, too
+        gg = sum_halves(sum_half(gg));
+        const float bound2 = gg * sum_halves(sum_half(vv + oo));
+        const int mine = min(bits_ahead(14 - kProb, bound2), bits_ahead(14, gg));
+        bits = -max_wave<0>(__builtin_amdgcn_readfirstlane(-mine));
         bits = max(min(bits, 15), -24);  // what one factor of fp16 can be
     }
     float up = power(bits);

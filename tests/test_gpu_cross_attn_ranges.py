@@ -153,6 +153,33 @@ def test_gradients_of_values_whose_output_cancels(rows, kind):
         assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
 
 
+@pytest.mark.parametrize("size", [1e-2, 1e-4, 3e-6, 300.0])
+@pytest.mark.parametrize("grad", [1e-3, 1.0, 50.0])
+def test_half_gradients_of_small_and_large_values(grad, size):
+    # the score gradients go with the product of the two sizes, and each has to fit the type as well.  The
+    # saved out is subnormal here for small values, so the reference takes delta from it, as the formula
+    # of the call does; then grad_q and grad_k carry their own rounding alone, grad_v that of the probabilities too
+    q, k, v, g = operands("f16", [90], [300], 2, 1, 64, 61, grad)
+    v = (v.float() * size).to(v.dtype)
+    qp, kp = index([0, 90]), index([0, 300])
+    out, lse = oeq.oeq_cross_attn_fwd(q, k, v, qp, kp)
+    got = oeq.oeq_cross_attn_bwd(q, k, v, qp, kp, out, lse, g)
+    Q, K, V, G, O = (host(t) for t in (q, k[:, 0], v[:, 0], g, out))
+    ref = [np.empty(Q.shape), np.zeros(K.shape), np.zeros(K.shape)]
+    for h in range(2):
+        S = 0.125 * Q[:, h] @ K.T
+        P = np.exp(S - S.max(1, keepdims=True))
+        P /= P.sum(1, keepdims=True)
+        dS = P * (G[:, h] @ V.T - (G[:, h] * O[:, h]).sum(1, keepdims=True))
+        ref[0][:, h] = 0.125 * dS @ K
+        ref[1] += 0.125 * dS.T @ Q[:, h]
+        ref[2] += P.T @ G[:, h]
+    for t, want, times in zip(got, ref, (1.35, 1.35, 1.75)):
+        own = rel_l2(rounded(want, "f16"), want)
+        e = rel_l2(host(t).reshape(want.shape), want)
+        assert e <= times * own + RTOL["f32"], (e, own)
+
+
 def test_half_gradients_of_bad_values_stay_with_their_rows():
     # NaN and infinite rows of grad_out reach every state of their structure and nothing else
     q, k, v, g = operands("f16", [70, 40], [90, 50], 2, 1, 32, 53)
