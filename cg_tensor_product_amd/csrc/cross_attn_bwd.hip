@@ -16,8 +16,9 @@
 // fp32 partial sums a second kernel adds in order.
 //
 // Bound by the vector unit next to the matrix unit, fp32 by its matrix instructions: 4 structures of
-// 1024 query rows and 2048 states, 8 heads over 4, D = 64: bf16 115 us (373 TFLOP/s of the minimal
-// products; 144 us with dropout, whose generator runs in both roles), fp32 483 us (89 TFLOP/s).
+// 1024 query rows and 2048 states, 8 heads over 4, D = 64: bf16 110 us (390 TFLOP/s of the minimal
+// products; 142 us with dropout, whose generator runs in both roles), fp16 113 and 143, fp32 485 us (89
+// TFLOP/s).
 //
 // The product that gives dp starts from -delta / (factor of what is kept) in its accumulators,
 // so that a score's gradient is one multiplication, and the factor is applied to the sums.
@@ -44,7 +45,7 @@ constexpr bool kExactDelta = sizeof(T) == 2;
 // the rest: rounded once, they and delta's rounding leave grad_q and grad_k with 1.4 to 1.9 times
 // the error that rounding the result alone does (10 to 4096 states), with the rest 1.0 to 1.2 from
 // 64 states on.  It costs 7 % of a decoder's training step (8 structures of up to 1024 query rows and
-// 2048 states, 8 heads over 4, D = 64, bf16, dropout: 224 -> 239 us).
+// 2048 states, 8 heads over 4, D = 64, bf16, dropout: 206 -> 221 us).
 template <class T>
 constexpr bool kRest = sizeof(T) == 2;
 
@@ -341,7 +342,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         for (int h = 0; h < 2; ++h) {
             // rows 16 h + 8 half + j of the tile; none: what dp - delta is where the probability was
             // dropped.  Read again here rather than kept, where that saves spills (D = 96 with dropout
-            // 240 -> 212 us; at D = 128, which spills either way, 342 -> 378).
+            // 228 -> 209 us; at D = 128, which spills either way, 341 -> 378).
             if (kDim < 128) asm volatile("" ::: "memory");
             const int first = 16 * h + 8 * half;
             f32x8 p8, s8, lse = load_lds8(lds.lse[buffer] + first), none;
@@ -616,10 +617,10 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 
 // Three workgroups a compute unit at D = 32 (fp16 with dropout, 64 structures of up to 32 rows and 200
 // states: 21.5 us for 25.0 with two), else two, where that does not leave too few registers: against one, D = 96
-// takes 165 us for 279 and D = 128 239 for 328 (bf16, 4 structures of 1024 query rows and 2048
-// states, 8 heads over 4); fp32 at D = 128 would take 1369 for 1102.
+// with dropout takes 209 us for 287 and D = 128 240 for 291 (bf16, 4 structures of 1024 query rows and 2048
+// states, 8 heads over 4); fp32 at D = 128 would take 1359 for 1029.
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
-__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 && kDim <= 32) ? 3 : (sizeof(T) == 2 || kDim <= 64) ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, (kScaled<T> && kDim <= 32) ? 3 : (sizeof(T) == 2 || kDim <= 64) ? 2 : 1)
     k_backward(AttnArgs a, Bwd out) {
     constexpr int kKeyBytes = int(sizeof(KeyLds<T, kDim>)), kQueryBytes = QueryTiles<T, kDim, kSplitKeys>::kBytes;
     __shared__ __attribute__((aligned(16))) char lds[kKeyBytes > kQueryBytes ? kKeyBytes : kQueryBytes];
@@ -699,8 +700,8 @@ int splits_of(int64_t walk, int64_t share) {
 Choice choose(const AttnArgs &a) {
     Choice c{};
     // Twice the workgroups the chip holds at once: walks half as long even out better than their
-    // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 107 us,
-    // 145 with walks of one round).
+    // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 111 us,
+    // 135 with walks of one round).
     const int64_t fill = 1024;
     c.split_keys = a.q_rows * a.share <= 32 * int64_t(a.n_struct);
     c.q_slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);

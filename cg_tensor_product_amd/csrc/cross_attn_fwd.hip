@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-// The running maximum may lag behind by this many powers of two before the sums are scaled.
+// The running maximum may lag behind by this many powers of two before the sums are scaled, so that most
+// tiles scale nothing (a device known from published attention kernels).
 constexpr float kLag = 8.f;
 
 template <class T, int kDim, bool kSplitKeys>
@@ -174,6 +175,8 @@ __global__ void __launch_bounds__(kThreads) k_forward(AttnArgs a, int splits, in
 #pragma unroll
                     for (int j = 0; j < 8; ++j) e[j] = (keep >> j & 1) ? e[j] : 0.f;
                 }
+                // 16-bit types round p once, as the product takes it: with that out has 1.3 to 1.4 times the
+                // error of rounding it alone; the rest as a second term would be half as many products more.
                 p[h] = from_f32<T>(e);
             }
 #pragma unroll
@@ -368,7 +371,10 @@ void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStrea
     // At 33 to 64 columns of a 16-bit type a compute unit would hold three workgroups, and with about
     // two for each some get three and some one.  LDS that nothing uses keeps them to two there (the
     // 512 workgroups above: 36 us for 43, with dropout 51 for 65; but 23 us for 17 where 768
-    // workgroups of 64 structures, many of them empty, can use the third place).
+    // workgroups of 64 structures, many of them empty, can use the third place).  The count has slots
+    // without rows in it, so the bound is a rough one: at 560 the two places win (4 x 384 rows: 27 us for 30), at
+    // 608 and 640 the three (4 x 1152: 44 for 53), and at 576 either does (4 x 512: 26 for 29 with two;
+    // 8 x 512: 43 for 49 with three).
     const unsigned spare = sizeof(T) == 2 && kDim == 64 && c.blocks <= 576 ? 20480 : 0;
     if (c.split_keys)
         k_forward<T, kDim, kDrop, true><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
