@@ -41,11 +41,12 @@ constexpr int kExactStates = 32;
 template <class T>
 constexpr bool kExactDelta = sizeof(T) == 2;
 
-// The score gradients of 16-bit types go into their products as two terms, the rounded value and
-// the rest: rounded once, they and delta's rounding leave grad_q and grad_k with 1.4 to 1.9 times
-// the error that rounding the result alone does (10 to 4096 states), with the rest 1.0 to 1.2 from
-// 64 states on.  It costs 7 % of a decoder's training step (8 structures of up to 1024 query rows and
-// 2048 states, 8 heads over 4, D = 64, bf16, dropout: 206 -> 221 us).
+// Probabilities and score gradients of 16-bit types go into their products as two terms, the rounded value
+// and the rest.  Rounded once, score gradients (with delta's rounding) leave grad_q and grad_k with 1.4 to 1.9
+// times the error that rounding the result alone does (10 to 4096 states), probabilities grad_v with 1.4
+// to 1.6 times; with the rest it is 1.0 to 1.2 from 64 states on.  For the score gradients that costs 7 % of a
+// decoder's training step (8 structures of up to 1024 query rows and 2048 states, 8 heads over 4, D = 64,
+// bf16, dropout: 206 -> 221 us), for the probabilities 5 to 8 % of the backward (159 -> 172 us there).
 template <class T>
 constexpr bool kRest = sizeof(T) == 2;
 
@@ -141,7 +142,7 @@ __device__ __forceinline__ float dot(vec8<T> a, vec8<T> b) {
     return v;
 }
 
-// Score gradients as operands of a product: the rounded values and the rest.
+// Probabilities or score gradients as operands of a product: the rounded values and the rest.
 template <class T>
 __device__ __forceinline__ void two_terms(f32x8 v, vec8<T> *value, vec8<T> *rest) {
     *value = from_f32<T>(v);
@@ -337,7 +338,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         for (int i = 0; i < kSteps; ++i) s = mma(s, row_operand(q_tile, kRow, row, 16 * i, half), kf[i]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) dp = mma(dp, row_operand(g_tile, kRow, row, 16 * i, half), vf[i]);
-        vec8<T> pf[2], sf[2], sl[2];
+        vec8<T> pf[2], pl[2], sf[2], sl[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             // rows 16 h + 8 half + j of the tile; none: what dp - delta is where the probability was
@@ -373,7 +374,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
                     s8[j] = p * dp[i];
                 }
             }
-            pf[h] = from_f32<T>(p8);
+            two_terms<T>(p8, &pf[h], &pl[h]);
             if (kScaled<T> && kCare) {
                 s8 *= up;
 #pragma unroll
@@ -392,7 +393,9 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                gv[d] = mma(gv[d], column_operand(g_tile, kRow, 16 * h, 32 * d, lane), pf[h]);
+                const vec8<T> g = column_operand(g_tile, kRow, 16 * h, 32 * d, lane);
+                gv[d] = mma(gv[d], g, pf[h]);
+                if (kRest<T>) gv[d] = mma(gv[d], g, pl[h]);
                 const vec8<T> q = column_operand(q_tile, kRow, 16 * h, 32 * d, lane);
                 gk[d] = mma(gk[d], q, sf[h]);
                 if (kRest<T>) gk[d] = mma(gk[d], q, sl[h]);

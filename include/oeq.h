@@ -541,9 +541,10 @@ oeq_status oeq_dropout_bwd(oeq_dtype dtype, int64_t n_rows, int64_t n_cols, cons
  * are never used, whatever they hold.
  *
  * One query row per structure (a serving step) to many, on any number of states, takes the
- * same call.  Of 16-bit types the probabilities are rounded to the type for their products; the
- * score gradients enter theirs as the rounded value and the rest.  In fp16 both are brought into
- * the type's range by powers of two, so only the operands and the results have to fit it. */
+ * same call.  Of 16-bit types the forward rounds the probabilities to the type for the product
+ * with v; in the backward they and the score gradients enter their products as the rounded value
+ * and the rest, in fp16 brought into the type's range by powers of two, so that only the operands
+ * and the results have to fit it. */
 typedef struct {
     oeq_dtype dtype;
     int32_t n_struct;

@@ -195,6 +195,18 @@ def test_half_gradients_of_bad_values_stay_with_their_rows():
         assert torch.equal(got["grad_v"][90:], clean["grad_v"][90:])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len,k_len", [([64], [96]), ([300], [9]), ([5, 40], [1000, 33])])
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_half_gradient_to_values_is_near_the_rounded_result(q_len, k_len, p, kind):
+    # nothing but the result is rounded to the type: its own error, and a tenth for the sample
+    q, k, v, g = operands(kind, q_len, k_len, 4, 2, 32, 67)
+    got, ref = both(q, k, v, g, q_len, k_len, p, (21, 22) if p else None)
+    own = rel_l2(rounded(ref["grad_v"], kind), ref["grad_v"])
+    e = rel_l2(host(got["grad_v"]), ref["grad_v"])
+    assert e <= 1.1 * own + RTOL["f32"], (e, own)
+
+
 # ---- structures of few states beside long ones ------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
