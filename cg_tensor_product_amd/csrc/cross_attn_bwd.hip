@@ -10,14 +10,14 @@
 // Both form delta themselves, from rows that they read anyway and from out.  Where out is
 // rounded to 16 bits and a structure has few states (kExactStates), that rounding would be
 // most of its gradients' error: there, in one tile of keys, delta is the sum of p dp in fp32.
-// Scores are formed twice (7 products of the minimal 5; 9 for 16-bit types with the second term of
-// the score gradients); the alternative, one walk that adds into grad_q, needs atomics or a partial
+// Scores are formed twice (7 products of the minimal 5; 10 for 16-bit types with the second terms of
+// probabilities and score gradients); the alternative, one walk that adds into grad_q, needs atomics or a partial
 // grad_q for each tile of keys.  With few workgroups the walks are split over workgroups, whose
 // fp32 partial sums a second kernel adds in order.
 //
 // Bound by the vector unit next to the matrix unit, fp32 by its matrix instructions: 4 structures of
-// 1024 query rows and 2048 states, 8 heads over 4, D = 64: bf16 110 us (390 TFLOP/s of the minimal
-// products; 142 us with dropout, whose generator runs in both roles), fp16 113 and 143, fp32 485 us (89
+// 1024 query rows and 2048 states, 8 heads over 4, D = 64: bf16 118 us (364 TFLOP/s of the minimal
+// products; 149 us with dropout, whose generator runs in both roles), fp16 120 and 150, fp32 482 us (89
 // TFLOP/s).
 //
 // The product that gives dp starts from -delta / (factor of what is kept) in its accumulators,
@@ -618,10 +618,10 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     }
 }
 
-// Three workgroups a compute unit at D = 32 (fp16 with dropout, 64 structures of up to 32 rows and 200
-// states: 21.5 us for 25.0 with two), else two, where that does not leave too few registers: against one, D = 96
-// with dropout takes 209 us for 287 and D = 128 240 for 291 (bf16, 4 structures of 1024 query rows and 2048
-// states, 8 heads over 4); fp32 at D = 128 would take 1359 for 1029.
+// Three workgroups a compute unit for fp16 at D = 32 (with dropout, 64 structures of up to 32 rows and 200
+// states: 21.5 us for 25.0 with two, before probabilities had two terms), else two, where that does not
+// leave too few registers: against one, D = 96 with dropout takes 209 us for 287 and D = 128 240 for 291 (bf16,
+// 4 structures of 1024 query rows and 2048 states, 8 heads over 4); fp32 at D = 128 would take 1359 for 1029.
 template <class T, int kDim, bool kDrop, bool kSplitKeys>
 __global__ void __launch_bounds__(kThreads, (kScaled<T> && kDim <= 32) ? 3 : (sizeof(T) == 2 || kDim <= 64) ? 2 : 1)
     k_backward(AttnArgs a, Bwd out) {
@@ -636,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, (kScaled<T> && kDim <= 32) ? 3 : (si
         if (!w.any) return;
         if (kExactDelta<T> && w.keys <= kExactStates) {
             grad_keys<T, kDim, kDrop, kExactDelta<T>, kScaled<T>>(a, out, w, tid, tiles);
-        } else if (!grad_keys<T, kDim, kDrop, false, false>(a, out, w, tid, tiles)) {
+        } else if ((kScaled<T> && w.rows <= kRowTile) || !grad_keys<T, kDim, kDrop, false, false>(a, out, w, tid, tiles)) {
+            // (a walk of one tile is done with care at once: fp16, 64 structures of up to 32 rows and 200
+            // states, D = 32 with dropout 21.2 -> 19.9 us)
             if constexpr (kScaled<T>) {
                 // finds its place and its thread anew: kept for this, they would take registers of the other walk
                 asm volatile("" : "+s"(block), "+v"(tid));
