@@ -12,15 +12,15 @@
 // Everything here is bound by memory.  A workgroup owns (part of a structure's rows, slab of
 // whole groups, about 64 channels): lanes run along the channels in pieces of eight, so a row of
 // the slab is one 128- or 256-byte access, and the sums over the rows are each thread's own until
-// one reduction at the end.  Structures of few rows are one part each, whose workgroup computes
-// the sums and then applies them (the second read comes from its cache); longer ones are cut into
-// tiles of rows, whose partial sums go through the workspace to a joining kernel, and a third one
-// applies them.  Tiles are as long in every structure, so the longest one sets no pace.  No
-// atomics: every result is bitwise repeatable.
+// one reduction at the end.  Structures of few rows on average are one part each, whose workgroup
+// computes the sums and then applies them (the second read comes from its cache), at the pace of the
+// longest; others are cut into tiles of rows, whose partial sums go through the workspace to a joining
+// kernel, and a third one applies them.  Tiles are as long in every structure, so there the longest one sets
+// no pace.  No atomics: every result is bitwise repeatable.
 //
-// 280000 x 256 in 32 uneven structures, bf16, SiLU (143 MB an operand): statistics 40 us, output 52
-// (5.5 TB/s), gradient sums 67 (4.3 TB/s, the vector unit three quarters busy), grad_x 77 (5.6 TB/s);
-// 100003 x 128, fp32: 12.9 and 18.7 us.  A few molecules are one kernel of 5 us, its loads' latency.
+// 280000 x 256 in 32 uneven structures, bf16, SiLU (143 MB an operand): statistics 39 us, output 51
+// (5.6 TB/s), gradient sums 69 (4.1 TB/s, the vector unit three quarters busy), grad_x 79 (5.5 TB/s);
+// 100003 x 128, fp32: 13.0 and 17.9 us.  A few molecules are one kernel of 6 us, its loads' latency.
 //
 // Sums are fp32 in a wave and fp64 from there on.  A thread sums squares about its own first row and moves
 // to the mean of what it has after 1, 2, 4, ... steps; threads and parts are joined by their means and squared
@@ -53,13 +53,15 @@ struct Shape {
     int64_t parts;
 };
 
-// One part a structure is two launches fewer, but goes at the longest structure's pace (SiLU, fp32,
-// forward and backward): 64 structures of 78 rows x 128 take 6.6 and 10.5 us, the like of 187 rows
-// 8.4 and 13.3, against 14.1 and 18.5 in tiles; with the same rows in uneven structures it is 87 and
-// 183 against 13.9 and 18.7.
-// The tile fills the chip once or twice over (forward and backward, fp32): 3000 rows x 128 take 11.5
-// and 13.8 us with tiles of 64 rows, 13.1 and 17.4 with 256; 100003 rows x 128 take 34.5 and 50.8
-// with 512, 37.1 and 55.9 with 256.
+// One part a structure is two launches fewer, but goes at the longest structure's pace (SiLU, fp32, forward
+// and backward of 128 channels): 64 structures of 78 rows take 6.6 and 10.5 us, the like of 187 rows 8.4 and
+// 13.3, against 14.1 and 18.5 in tiles; 64 structures of which one has 7937 of 8000 rows take 81 and 170, and
+// would take the same 14 and 19 in tiles.  The host knows the average alone, and up to it even batches are the
+// usual ones.
+// The tile fills the chip once or twice over (forward and backward, fp32, 128 channels; work is two for a row):
+// 3000 rows take 11.5 and 13.8 us with tiles of 64 rows, 13.1 and 17.4 with 256; 48000 take 25.1 and 33.9
+// with 128, 24.0 and 32.3 with 256, 28.6 and 40.7 with 64; 80000 take 31.3 and 42.5 with 256, 32.2 and 46.4
+// with 512; 160000 take 49.0 and 73.6 with 256, 48.3 and 71.4 with 512.
 Shape shape_of(int64_t rows, int32_t n_struct, int32_t channels, int32_t groups) {
     Shape s;
     s.cg = channels / groups;
