@@ -393,9 +393,9 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const vec8<T> g = column_operand(g_tile, kRow, 16 * h, 32 * d, lane);
-                gv[d] = mma(gv[d], g, pf[h]);
-                if (kRest<T>) gv[d] = mma(gv[d], g, pl[h]);
+                const vec8<T> go = column_operand(g_tile, kRow, 16 * h, 32 * d, lane);
+                gv[d] = mma(gv[d], go, pf[h]);
+                if (kRest<T>) gv[d] = mma(gv[d], go, pl[h]);
                 const vec8<T> q = column_operand(q_tile, kRow, 16 * h, 32 * d, lane);
                 gk[d] = mma(gk[d], q, sf[h]);
                 if (kRest<T>) gk[d] = mma(gk[d], q, sl[h]);
@@ -497,6 +497,10 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 #pragma unroll
         for (int d = 0; d < kOut; ++d) gq[d] = f32x16{};
         const float p_lse = lse - (kScaled<T> ? float(bits) : 0.f);
+        if (!kSplitKeys) {  // every walk starts with the first buffer, as the count of its tiles does
+            k_tile = reinterpret_cast<T *>(lds);
+            v_tile = k_tile + C::kTile;
+        }
         for (int t = t_begin, buffer = 0; t < t_end; t += t_step) {
             if (kSplitKeys) wave_sync();
             const uint64_t valid = in.store(k_tile, v_tile);
