@@ -58,14 +58,14 @@ constexpr bool kRest = sizeof(T) == 2;
 //   grad_keys     one for the workgroup: p carries 2^kProbBits (of it grad_v too: probabilities near
 //                 2^-16 would keep eight bits, and keep all), the rows of grad_out in LDS the rest.
 // Where a walk meets rows so much larger that a score gradient passes 65504, its sums are no longer
-// finite, and it is done again: that of queries 2^24 lower for the rows concerned, up to kTries times (enough
-// for any fp16 inputs), that of keys with care (kCare): a power for each key, from 2^60 on, falls
+// finite (as where an input is not), and it is done again: that of queries with the powers that a walk for
+// the largest of each row finds, that of keys with care (kCare): a power for each key, from 2^60 on, falls
 // with the tile whose largest reaches 2 so that this one gets 2^-6 .. 2^-5, and the sums are scaled along;
 // what is lost is below 2^-19 of the column's largest.  With care from the start large calls take
 // 10 % longer (D = 64: each tile waits for the check).
 template <class T>
 constexpr bool kScaled = std::is_same<T, f16>::value;
-constexpr int kTries = 5, kLower = 24, kCareBits = 60;
+constexpr int kCareBits = 60;
 template <class T, bool kCare>
 constexpr int kProbBits = kScaled<T> ? (kCare ? 15 : 6) : 0;
 
@@ -74,6 +74,11 @@ __device__ __forceinline__ float power(int bits) { return __builtin_ldexpf(1.f, 
 // The power that puts a bound, given its square (0: not known), between 2^(to - 1) and 2^to.
 __device__ __forceinline__ int bits_ahead(int to, float bound2) {
     return bound2 > 0.f ? to - ((__builtin_amdgcn_frexp_expf(bound2) + 1) >> 1) : 0;
+}
+
+// The power that brings the largest of a row between 2^13 and 2^14.
+__device__ __forceinline__ int bits_for(float most) {
+    return most > 0.f ? max(14 - __builtin_amdgcn_frexp_expf(most), -100) : 0;
 }
 
 // Whether all sums are finite (they are far from where their own sum would not be).
@@ -493,10 +498,11 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     f32x16 gq[kOut];
     int bits = kScaled<T> && !kExact ? bits_ahead(14, sum_halves(gg) * sum_halves(oo)) : 0;  // the power of gq
 
-    for (int tries = 1;; ++tries) {
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) gq[d] = f32x16{};
-        const float p_lse = lse - (kScaled<T> ? float(bits) : 0.f);
+    // kMost: for the largest score gradient of each row alone, without the power
+    float most = 0.f;
+    const auto walk = [&](auto kind) {
+        constexpr bool kMost = decltype(kind)::value;
+        const float p_lse = lse - (kScaled<T> && !kMost ? float(bits) : 0.f);
         if (!kSplitKeys) {  // every walk starts with the first buffer, as the count of its tiles does
             k_tile = reinterpret_cast<T *>(lds);
             v_tile = k_tile + C::kTile;
@@ -537,8 +543,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
                     f32x16 ds;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) ds[i] = probability<T>(s[i], a.scale, c, lse) * dp[i];
-                    const float most = largest(ds);
-                    bits = most > 0.f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
+                    bits = bits_for(largest(ds));
                     dp *= power(bits);
                 }
             }
@@ -549,16 +554,19 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
                 for (int j = 0; j < 8; ++j) {
                     const float p = probability<T>(s[8 * h + j], a.scale, c, kExact ? lse : p_lse);
                     s8[j] = p * (kExact || !kDrop || (keep[h] & (1u << j)) ? dp[8 * h + j] : none);
+                    if (kMost) most = fmaxf(most, fabsf(s8[j]));
                 }
-                two_terms<T>(s8, &sf[h], &sl[h]);
+                if (!kMost) two_terms<T>(s8, &sf[h], &sl[h]);
             }
+            if constexpr (!kMost) {
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) {
+                for (int d = 0; d < kOut; ++d) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
-                    gq[d] = mma(gq[d], k, sf[h]);
-                    if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
+                    for (int h = 0; h < 2; ++h) {
+                        const vec8<T> k = column_operand(k_tile, kRow, 16 * h, 32 * d, lane);
+                        gq[d] = mma(gq[d], k, sf[h]);
+                        if (kRest<T>) gq[d] = mma(gq[d], k, sl[h]);
+                    }
                 }
             }
             if (!kSplitKeys) {
@@ -566,10 +574,20 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
                 v_tile = k_tile + C::kTile;
             }
         }
+    };
+    for (bool again = false;; again = true) {
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) gq[d] = f32x16{};
+        walk(std::false_type());
         if constexpr (!kScaled<T> || kExact) break;
-        const bool again = !finite(gq), any = __any(again);
-        if (!(kSplitKeys ? any : max_wave<2>(any)) || tries == kTries) break;
-        if (again) bits -= kLower;
+        const bool lost = max_halves(finite(gq) ? 0.f : 1.f) > 0.f;  // the row, whose columns are in both halves
+        const int any = __any(lost);
+        if (again || !(kSplitKeys ? any : max_wave<2>(any))) break;
+        in.fetch(a, k_base, v_base, mask, w.keys, t_begin);
+        walk(std::true_type());
+        most = max_halves(most);
+        if (lost) bits = bits_for(most);
+        if (!kSplitKeys) __syncthreads();  // before the first buffer is written again
         in.fetch(a, k_base, v_base, mask, w.keys, t_begin);
     }
     if (kScaled<T>) {

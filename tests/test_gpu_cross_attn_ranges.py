@@ -299,6 +299,28 @@ def test_gradients_of_states_with_minus_infinite_scores(q_len, k_len, kind):
         assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("q_len,k_len", [([5], [70]), ([150], [90]), ([40, 3], [33, 200])])
+def test_gradients_beside_one_infinite_column_of_the_states(q_len, k_len, kind):
+    # every fifth state is unseen by -infinity in one column: grad_q is NaN there, zero times infinity, and in
+    # the other columns what it is without these states
+    q, k, v, g = operands(kind, q_len, k_len, 2, 1, 32, 73)
+    q[..., 3] = q[..., 3].abs() + 0.125
+    mask = torch.ones(k.shape[0], dtype=torch.uint8, device="cuda")
+    mask[::5] = 0
+    _, ref = both(q, k, v, g, q_len, k_len, mask=mask)
+    k[::5, :, 3] = -float("inf")
+    qp, kp = index(ptr(q_len)), index(ptr(k_len))
+    out, lse = oeq.oeq_cross_attn_fwd(q, k, v, qp, kp)
+    got = dict(zip(("grad_q", "grad_k", "grad_v"), oeq.oeq_cross_attn_bwd(q, k, v, qp, kp, out, lse, g)))
+    others = [c for c in range(32) if c != 3]
+    u = {"f32": 0.0, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    assert torch.isnan(got["grad_q"][..., 3]).all()
+    assert rel_l2(host(got["grad_q"])[..., others], ref["grad_q"][..., others]) <= 4 * u + RTOL["f32"]
+    for n in ("grad_k", "grad_v"):
+        assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
+
+
 # ---- the call's own numbers ---------------------------------------------------------------------------
 
 def test_scale_and_probability_are_read_at_each_call():
