@@ -65,7 +65,7 @@ constexpr bool kRest = sizeof(T) == 2;
 // 10 % longer (D = 64: each tile waits for the check).
 template <class T>
 constexpr bool kScaled = std::is_same<T, f16>::value;
-constexpr int kCareBits = 60;
+constexpr int kMostBits = 60;  // what is below 2^-60 is nothing to a result, and no product with it overflows fp32
 template <class T, bool kCare>
 constexpr int kProbBits = kScaled<T> ? (kCare ? 15 : 6) : 0;
 
@@ -73,12 +73,12 @@ __device__ __forceinline__ float power(int bits) { return __builtin_ldexpf(1.f, 
 
 // The power that puts a bound, given its square (0: not known), between 2^(to - 1) and 2^to.
 __device__ __forceinline__ int bits_ahead(int to, float bound2) {
-    return bound2 > 0.f ? to - ((__builtin_amdgcn_frexp_expf(bound2) + 1) >> 1) : 0;
+    return bound2 > 0.f ? min(to - ((__builtin_amdgcn_frexp_expf(bound2) + 1) >> 1), kMostBits) : 0;
 }
 
 // The power that brings the largest of a row between 2^13 and 2^14.
 __device__ __forceinline__ int bits_for(float most) {
-    return most > 0.f ? max(14 - __builtin_amdgcn_frexp_expf(most), -100) : 0;
+    return most > 0.f ? min(14 - __builtin_amdgcn_frexp_expf(most), kMostBits) : 0;
 }
 
 // Whether all sums are finite (they are far from where their own sum would not be).
@@ -273,7 +273,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
     const float c = a.scale * kLog2E, start = -1.f / a.keep_scale;
     f32x16 gk[kOut] = {}, gv[kOut] = {};
     constexpr int kProb = kProbBits<T, kCare>;
-    int bits = kScaled<T> && kCare ? kCareBits - kProb : 0;  // with kProb the power of gk; not kCare: of grad_out
+    int bits = kScaled<T> && kCare ? kMostBits - kProb : 0;  // with kProb the power of gk; not kCare: of grad_out
     if constexpr (kScaled<T> && !kCare) {
         // the rows that this wave brings for the first tile stand for all
         float gg = 0.f, oo = 0.f, vv = 0.f;

@@ -321,6 +321,31 @@ def test_gradients_beside_one_infinite_column_of_the_states(q_len, k_len, kind):
         assert rel_l2(host(got[n]), ref[n]) <= 4 * u + RTOL["f32"], n
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("states", [2, 20, 32, 33, 200])
+@pytest.mark.parametrize("gap", [20.0, 80.0, 84.0, 86.0, 87.0, 110.0])
+@pytest.mark.parametrize("low", [0.0, -1.0])
+def test_gradients_of_rows_that_see_one_state(low, gap, states, kind):
+    # the other states' probabilities are e^-gap, down to below the normal fp32 numbers, and so are all score
+    # gradients: nothing that fp16 holds, and nothing that is not finite.  With one probability within 2^-24 of one,
+    # (dP - delta) is the rounding of a sum of size 10 in 16-bit types (and of the saved out): 4 u of it
+    r = np.random.default_rng(79)
+    q = torch.zeros((40, 2, 32), dtype=TYPES[kind], device="cuda")
+    k = torch.from_numpy(r.normal(size=(states, 1, 32))).to("cuda", TYPES[kind])
+    q[..., 0], k[..., 0] = 8.0, low * gap
+    k[states // 2, 0, 0] = (low + 1.0) * gap  # at a score of zero its probability is one without rounding
+    v, g = (torch.from_numpy(r.normal(size=s)).to("cuda", TYPES[kind]) for s in (k.shape, q.shape))
+    args = (q, k, v, index([0, 40]), index([0, states]))
+    out, lse = oeq.oeq_cross_attn_fwd(*args, scale=0.125)
+    got = oeq.oeq_cross_attn_bwd(*args, out, lse, g, scale=0.125)
+    ref = readout.cross_attn(host(q), host(k), host(v), [0, 40], [0, states], 0.125, grad_out=host(g))
+    u = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind]
+    assert rel_l2(host(got[2]), ref["grad_v"]) <= 4 * u + RTOL["f32"]
+    # scale |k| u |dP| a row, over 40 rows and 2 heads for grad_k
+    assert np.abs(host(got[0]) - ref["grad_q"]).max() <= 0.125 * gap * 4 * u * 20 + 1e-3
+    assert np.abs(host(got[1]) - ref["grad_k"]).max() <= 0.125 * 8 * 80 * 4 * u * 20 + 1e-3
+
+
 # ---- the call's own numbers ---------------------------------------------------------------------------
 
 def test_scale_and_probability_are_read_at_each_call():
