@@ -38,7 +38,9 @@ EXPORTED = ["oeq_plan_create", "oeq_plan_create_cached", "oeq_plan_destroy", "oe
             "oeq_radial_bwd", "oeq_tp_conv_fwd_radial", "oeq_workspace_size_radial", "oeq_tp_conv_bwd_radial",
             "oeq_tp_conv_fwd_pos", "oeq_workspace_size_pos", "oeq_tp_conv_bwd_pos",
             "oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
-            "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd"]
+            "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd",
+            "oeq_embedding_fwd", "oeq_embedding_workspace_size", "oeq_embedding_bwd", "oeq_rms_norm_workspace_size",
+            "oeq_rms_norm_fwd", "oeq_rms_norm_bwd"]
 SCHEDULES = {0: "receiver", 1: "sender"}
 
 
@@ -174,6 +176,18 @@ def lib():
     L.oeq_cross_attn_fwd.restype = st
     L.oeq_cross_attn_bwd.argtypes = [AD] + [P] * 14 + [SZ, P]
     L.oeq_cross_attn_bwd.restype = st
+    L.oeq_embedding_fwd.argtypes = [I, I64, I64, I64, P, I64, P, I32, D, P, I64, P]
+    L.oeq_embedding_fwd.restype = st
+    L.oeq_embedding_workspace_size.argtypes = [I, I64, I64, I64, SZP]
+    L.oeq_embedding_workspace_size.restype = st
+    L.oeq_embedding_bwd.argtypes = [I, I64, I64, I64, P, I32, D, P, I64, P, I64, P, SZ, P]
+    L.oeq_embedding_bwd.restype = st
+    L.oeq_rms_norm_workspace_size.argtypes = [I64, I32, SZP]
+    L.oeq_rms_norm_workspace_size.restype = st
+    L.oeq_rms_norm_fwd.argtypes = [I, I64, I32, D, P, I64, P, I64, P, P, I64, P, I64, P, P, P]
+    L.oeq_rms_norm_fwd.restype = st
+    L.oeq_rms_norm_bwd.argtypes = [I, I64, I32, P, I64, P, P, P, I64, P, I64, P, I64, P, P, SZ, P]
+    L.oeq_rms_norm_bwd.restype = st
     L.oeq_status_string.argtypes = [ctypes.c_int]
     L.oeq_status_string.restype = ctypes.c_char_p
     L.oeq_last_error.argtypes = []
@@ -725,17 +739,23 @@ def oeq_tp_conv_bwd_radial(plan: Plan, rowptr, src, x, Y, vec, r_cut: float, W1,
 
 
 # ---------------------------------------------------------------------------
-# readout operators (readout.py), loaded on first use: they need torch at import
+# readout and decoder operators (readout.py, decoder.py), loaded on first use: they need torch at import
 # ---------------------------------------------------------------------------
 
-_READOUT = ("oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
-            "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd")
+_LATER = {
+    "readout": ("oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
+                "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd"),
+    "decoder": ("oeq_embedding_fwd", "oeq_embedding_workspace_size", "oeq_embedding_bwd", "oeq_rms_norm_workspace_size",
+                "oeq_rms_norm_fwd", "oeq_rms_norm_e4m3_fwd", "oeq_rms_norm_bwd"),
+}
 
 
 def __getattr__(name):
-    if name not in _READOUT:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import readout
-    for n in _READOUT:
-        globals()[n] = getattr(readout, n)
-    return globals()[name]
+    for module, names in _LATER.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -20,9 +20,10 @@ LIB = os.path.join(PKG, "liboeq.so")
 JITC = os.path.join(PKG, "oeq_jitc")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
-HOST_SOURCES = ["capi.cpp", "capi_graph.cpp", "capi_edge.cpp", "capi_readout.cpp", "planner.cpp", "cg_tables.cpp", "codegen.cpp",
-                "jit.cpp"]
-HIP_SOURCES = ["csr.hip", "noalloc.hip", "group_norm.hip", "dropout.hip", "cross_attn_fwd.hip", "cross_attn_bwd.hip"]
+HOST_SOURCES = ["capi.cpp", "capi_graph.cpp", "capi_edge.cpp", "capi_readout.cpp", "capi_decoder.cpp",
+                "planner.cpp", "cg_tables.cpp", "codegen.cpp", "jit.cpp"]
+HIP_SOURCES = ["csr.hip", "noalloc.hip", "group_norm.hip", "dropout.hip", "cross_attn_fwd.hip", "cross_attn_bwd.hip",
+               "embedding.hip", "rms_norm.hip"]
 ARCH = "gfx950"
 # Accumulators of the matrix instructions in ordinary registers: the vector code between two
 # products then reads them in place.  With the default form the attention kernels moved hundreds

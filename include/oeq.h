@@ -81,8 +81,8 @@ typedef enum {
     OEQ_ERR_JIT = 5          /* runtime compilation of the kernels failed    */
 } oeq_status;
 
-/* Plans take OEQ_F32 and OEQ_F64; the readout operators (below) OEQ_F32, OEQ_F16 and
- * OEQ_BF16. */
+/* Plans take OEQ_F32 and OEQ_F64; the readout and decoder operators (below)
+ * OEQ_F32, OEQ_F16 and OEQ_BF16. */
 typedef enum { OEQ_F32 = 0, OEQ_F64 = 1, OEQ_F16 = 2, OEQ_BF16 = 3 } oeq_dtype;
 
 /* How the x gradient is scattered to senders in the backward passes.
@@ -579,6 +579,63 @@ oeq_status oeq_cross_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, c
                               const int64_t *rng, const void *out, const float *lse,
                               const void *grad_out, void *grad_q, void *grad_k, void *grad_v,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Decoder operators ---------------------------------------------------------
+ * What a decoder over structures needs next to the cross attention to their states: tokens
+ * (or the atoms' species) as rows of a table, the norm of the residual stream, and the causal
+ * attention among the tokens.  The conventions of the readout operators hold: fp32, fp16 and
+ * bf16, 32-bit sums or longer, strides in elements, no allocation, no floating-point atomics,
+ * so every result is bitwise repeatable. */
+
+/* Embedding lookup: out[i] = scale table[index[i]] for i < n_rows, rows of n_cols elements;
+ * index is int32 or int64 (index_bytes 4 or 8).  An index outside [0, n_table) names no row:
+ * it gives a row of zeros and takes no gradient (padding is index -1). */
+oeq_status oeq_embedding_fwd(oeq_dtype dtype, int64_t n_table, int64_t n_cols, int64_t n_rows,
+                             const void *table, int64_t table_stride, const void *index,
+                             int32_t index_bytes, double scale, void *out, int64_t out_stride,
+                             void *stream);
+
+/* Its gradient to the table: grad_table[t] = scale times the sum of grad_out[i] over the rows i
+ * with index[i] = t, summed in an order that depends on the index alone and rounded once; rows
+ * that no index names are zeroed.  `workspace` of oeq_embedding_workspace_size bytes. */
+oeq_status oeq_embedding_workspace_size(oeq_dtype dtype, int64_t n_table, int64_t n_cols,
+                                        int64_t n_rows, size_t *bwd_bytes);
+oeq_status oeq_embedding_bwd(oeq_dtype dtype, int64_t n_table, int64_t n_cols, int64_t n_rows,
+                             const void *index, int32_t index_bytes, double scale,
+                             const void *grad_out, int64_t grad_out_stride, void *grad_table,
+                             int64_t grad_table_stride, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Root-mean-square norm of rows of n_cols <= 16384 elements, with the residual's addition:
+ *   h = x + residual, rounded to dtype and written to `sum`: the residual stream
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd weight[c]
+ * residual NULL: h = x, and `sum` is not written.  weight is fp32, NULL for ones.  out_scale
+ * NULL: out has dtype.  Otherwise out holds e4m3 (4 exponent bits, 3 of mantissa, largest value
+ * 448; one byte each, out_stride in bytes) of y / scale with a scale for each row, written to
+ * out_scale: scale = max(largest |y| of the row, 2^-100) / 448.  A row that holds a NaN or an
+ * infinity has a scale that is not finite or values that are NaN.  rstd (fp32 [n_rows]) is
+ * written for the backward where it is not NULL.  `sum` may be x or residual itself (the stream
+ * updated in place).  eps > 0. */
+oeq_status oeq_rms_norm_fwd(oeq_dtype dtype, int64_t n_rows, int32_t n_cols, double eps,
+                            const void *x, int64_t x_stride, const void *residual,
+                            int64_t residual_stride, const float *weight, void *sum,
+                            int64_t sum_stride, void *out, int64_t out_stride, float *out_scale,
+                            float *rstd, void *stream);
+
+/* Gradients of <grad_out, y> + <grad_sum, h>, from h (`sum`: the forward's sum, or its x) and
+ * rstd: with hat = h rstd and dy = grad_out weight,
+ *   grad_x = rstd (dy - hat mean(dy hat)) + grad_sum, the gradient to x and to the residual
+ *   grad_weight = sum over the rows of grad_out hat (fp32 [n_cols])
+ * grad_sum (what arrives at the residual stream past the norm) may be NULL, and so may either
+ * gradient (not computed).  grad_x may be grad_out or grad_sum itself.  `workspace` of
+ * oeq_rms_norm_workspace_size bytes is needed for grad_weight. */
+oeq_status oeq_rms_norm_workspace_size(int64_t n_rows, int32_t n_cols, size_t *bwd_bytes);
+oeq_status oeq_rms_norm_bwd(oeq_dtype dtype, int64_t n_rows, int32_t n_cols, const void *sum,
+                            int64_t sum_stride, const float *weight, const float *rstd,
+                            const void *grad_out, int64_t grad_out_stride, const void *grad_sum,
+                            int64_t grad_sum_stride, void *grad_x, int64_t grad_x_stride,
+                            float *grad_weight, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /* Synchronously validates a receiver CSR on the device (rowptr monotone,
  * rowptr[0] = 0, rowptr[N] = E, 0 <= src < N).  Test helper: synchronises. */

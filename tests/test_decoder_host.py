@@ -1,0 +1,109 @@
+"""Host-side checks of the decoder operators' C ABI (no GPU needed): every refusal comes back as a
+status code before any device work, and workspace sizes are functions of the shapes."""
+import ctypes
+
+import pytest
+
+oeq = pytest.importorskip("cg_tensor_product_amd")
+
+P = ctypes.c_void_p
+A = P(4096)  # an address that is never followed: the calls below stop before any device work
+
+
+def _message():
+    return oeq.lib().oeq_last_error().decode()
+
+
+# ---- embedding ----------------------------------------------------------------------------
+
+def _emb(dtype=0, table=5, cols=8, rows=4, t=A, ld_t=8, index=A, size=8, scale=1.0, out=A, ld_o=8):
+    return oeq.lib().oeq_embedding_fwd(dtype, table, cols, rows, t, ld_t, index, size, scale, out, ld_o, None)
+
+
+def _emb_bwd(dtype=0, table=5, cols=8, rows=4, index=A, size=8, scale=1.0, go=A, ld_go=8, gt=A, ld_gt=8, ws=A,
+             wsb=1 << 20):
+    return oeq.lib().oeq_embedding_bwd(dtype, table, cols, rows, index, size, scale, go, ld_go, gt, ld_gt, ws, wsb, None)
+
+
+SHARED = [
+    (dict(dtype=1), 2), (dict(dtype=9), 2), (dict(table=-1), 1), (dict(cols=-1), 1), (dict(rows=-1), 1),
+    (dict(table=2**31 - 1), 2), (dict(rows=2**31 - 1), 2), (dict(cols=2**31 - 1), 2), (dict(size=2), 1), (dict(size=0), 1),
+    (dict(index=None), 1), (dict(index=P(4100)), 1), (dict(index=P(4098), size=4), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=1e300), 1),
+]
+
+
+@pytest.mark.parametrize("kw,status", SHARED + [
+    (dict(t=None), 1), (dict(out=None), 1), (dict(ld_t=7), 1), (dict(ld_o=7), 1), (dict(t=P(4098)), 1),
+    (dict(out=P(4097), dtype=2), 1),
+])
+def test_embedding_refusals(kw, status):
+    assert _emb(**kw) == status, _message()
+
+
+@pytest.mark.parametrize("kw,status", SHARED + [
+    (dict(go=None), 1), (dict(gt=None), 1), (dict(ld_go=7), 1), (dict(ld_gt=7), 1), (dict(go=P(4098)), 1),
+    (dict(gt=P(4097), dtype=3), 1), (dict(ws=None), 3), (dict(wsb=31), 3), (dict(ws=P(4104)), 3),
+])
+def test_embedding_backward_refusals(kw, status):
+    assert _emb_bwd(**kw) == status, _message()
+
+
+def test_embedding_empty_calls_do_nothing():
+    assert _emb(rows=0, index=None, out=None, t=None) == 0 and _emb(cols=0, out=None, t=None) == 0
+    assert _emb_bwd(table=0, gt=None) == 0 and _emb_bwd(cols=0, gt=None, ws=None) == 0
+
+
+def test_embedding_workspace_sizes():
+    b = ctypes.c_size_t()
+    size = oeq.lib().oeq_embedding_workspace_size
+    assert size(0, 100, 64, 0, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(0, 100, 64, 10, ctypes.byref(b)) == 0 and b.value >= 2 * 10 * 4  # keys and positions
+    assert size(0, 1 << 20, 64, 10**6, ctypes.byref(b)) == 0 and b.value >= 4 * 10**6 * 4
+    assert size(0, 0, 64, 10, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(0, 100, 64, 10, None) == 0
+    assert size(0, 2**31 - 2, 2**31 - 2, 10, ctypes.byref(b)) == 2  # a launch of too many workgroups
+
+
+# ---- rms norm -------------------------------------------------------------------------------
+
+def _rms(dtype=0, rows=3, cols=8, eps=1e-5, x=A, ld=8, res=None, ld_r=0, w=None, s=None, ld_s=0, out=A, ld_o=8,
+         scale=None, rstd=A):
+    return oeq.lib().oeq_rms_norm_fwd(dtype, rows, cols, eps, x, ld, res, ld_r, w, s, ld_s, out, ld_o, scale, rstd, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=1), 2), (dict(rows=-1), 1), (dict(cols=0), 1), (dict(cols=16385), 2), (dict(rows=2**40), 2),
+    (dict(eps=0.0), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
+    (dict(eps=1e-60), 1), (dict(x=None), 1), (dict(out=None), 1), (dict(ld=7), 1), (dict(ld_o=7), 1),
+    (dict(x=P(4098)), 1), (dict(out=P(4098)), 1), (dict(w=P(4098)), 1), (dict(rstd=P(4098)), 1),
+    (dict(scale=P(4097)), 1), (dict(res=A, ld_r=8), 1), (dict(res=A, ld_r=7, s=A, ld_s=8), 1),
+    (dict(res=A, ld_r=8, s=A, ld_s=7), 1), (dict(res=P(4098), ld_r=8, s=A, ld_s=8), 1),
+    (dict(res=A, ld_r=8, s=P(4098), ld_s=8), 1),
+])
+def test_rms_norm_refusals(kw, status):
+    assert _rms(**kw) == status, _message()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=1), 2), (dict(cols=0), 1), (dict(cols=16385), 2), (dict(s=None), 1), (dict(go=None), 1),
+    (dict(rstd=None), 1), (dict(ld_s=7), 1), (dict(ld_go=7), 1), (dict(gs=A, ld_gs=7), 1), (dict(ld_gx=7), 1),
+    (dict(gx=P(4098)), 1), (dict(gw=P(4098)), 1), (dict(w=P(4098)), 1), (dict(ws=None), 3), (dict(wsb=31), 3),
+    (dict(ws=P(4104)), 3), (dict(gx=None, gw=None), 0), (dict(rows=0, s=None, go=None, rstd=None, gx=None, gw=None), 0),
+])
+def test_rms_norm_backward_refusals(kw, status):
+    k = {**dict(dtype=0, rows=3, cols=8, s=A, ld_s=8, w=None, rstd=A, go=A, ld_go=8, gs=None, ld_gs=0, gx=A, ld_gx=8,
+                gw=A, ws=A, wsb=1 << 20), **kw}
+    assert oeq.lib().oeq_rms_norm_bwd(*k.values(), None) == status, _message()
+
+
+def test_rms_norm_empty_calls_do_nothing():
+    assert _rms(rows=0, x=None, out=None, rstd=None) == 0
+
+
+def test_rms_norm_workspace_sizes():
+    b = ctypes.c_size_t()
+    size = oeq.lib().oeq_rms_norm_workspace_size
+    assert size(0, 64, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(10, 4096, ctypes.byref(b)) == 0 and b.value >= 4096 * 4
+    assert size(10, 0, ctypes.byref(b)) == 1 and size(-1, 8, None) == 1 and size(10, 16385, None) == 2
