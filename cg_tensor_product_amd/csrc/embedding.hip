@@ -4,14 +4,15 @@
 //
 // The lookup is a copy of rows: a thread takes eight columns of one.
 //
-// The gradient's sums have no atomics: (index, position) pairs are sorted by index with the positions of
+// The gradient's sums have no atomics.  (index, position) pairs are sorted by index with the positions of
 // one index in increasing order (a stable radix sort), the sorted list is cut into chunks of equal
 // length, and a few lanes walk each chunk, their columns in registers, and write a table row where
-// its run of equal indices ends.  So neither a common index (tens of thousands of uses of one species)
-// nor many rare ones (a vocabulary) leave lanes idle.  A run that a cut divides leaves a partial sum a
-// chunk, and a second kernel adds those in order.  Rows that no index names are zeroed by further
-// workgroups of the same launch, which look for their rows in the sorted list.
+// its run of equal indices ends.  So neither a common index (thousands of uses of one species) nor
+// many rare ones (a vocabulary) leave lanes idle.  A run that a cut divides leaves a partial sum a
+// chunk, and a second kernel adds those in order.  Rows that no index names are zeroed by workgroups
+// of the sorting launches, and tables of few rows need no sort (k_small).
 #include <algorithm>
+#include <type_traits>
 
 #include "readout.hpp"
 #include "readout_device.hpp"
@@ -22,6 +23,7 @@ namespace readout {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr uint32_t kNone = ~0u;
 
 template <class T>
 __device__ __forceinline__ vec8<T> load_cols(const T *p, int n) {
@@ -35,10 +37,26 @@ __device__ __forceinline__ void store_cols(T *p, vec8<T> v, int n) {
         store_part(p, v, n);
 }
 
-// The table row that index i names, or `none`.
-__device__ __forceinline__ int64_t index_at(const EmbeddingArgs &a, int64_t i, int64_t none) {
-    const int64_t t = a.wide ? static_cast<const int64_t *>(a.index)[i] : static_cast<const int32_t *>(a.index)[i];
-    return t >= 0 && t < a.table_rows ? t : none;
+// The table row that index i names, or `none`.  A 64-bit index is read as two words and both widths take
+// the same loads, without a branch: a value that comes by two ways is waited for where they meet,
+// and no two loads of a thread would overlap.
+__device__ __forceinline__ uint32_t index_at(const EmbeddingArgs &a, int64_t i, uint32_t none) {
+    const uint32_t *at = static_cast<const uint32_t *>(a.index) + (i << a.wide);
+    const uint32_t low = at[0], high = at[a.wide] & (a.wide ? ~0u : 0u);
+    return (low < static_cast<uint32_t>(a.table_rows)) & (high == 0) ? low : none;
+}
+
+// The first n of eight (or kW) columns, 0 < n; the others are zero.  All loads are made, as above.
+template <class Vec, class T>
+__device__ __forceinline__ Vec load_first(const T *p, int n) {
+    constexpr int kW = sizeof(Vec) / sizeof(T);
+    Vec v;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+        const T x = p[min(k, n - 1)];
+        v[k] = k < n ? x : T(0.f);
+    }
+    return v;
 }
 
 // ---- lookup ---------------------------------------------------------------------------
@@ -50,9 +68,9 @@ __global__ void __launch_bounds__(kThreads) k_lookup(EmbeddingArgs a, uint32_t p
         const Index row = i / per_row;
         const int64_t col = int64_t(i - row * per_row) * 8;
         const int n = static_cast<int>(min(a.cols - col, int64_t(8)));
-        const int64_t t = index_at(a, static_cast<int64_t>(row), -1);
+        const uint32_t t = index_at(a, static_cast<int64_t>(row), kNone);
         f32x8 v = {};
-        if (t >= 0) v = to_f32<T>(load_cols(static_cast<const T *>(a.table) + t * a.ld_table + col, n)) * a.scale;
+        if (t != kNone) v = to_f32<T>(load_cols(static_cast<const T *>(a.table) + t * a.ld_table + col, n)) * a.scale;
         store_cols(static_cast<T *>(a.out) + static_cast<int64_t>(row) * a.ld_out + col, from_f32<T>(v), n);
         if (total - i <= step) break;  // before i + step can wrap
     }
@@ -70,21 +88,152 @@ hipError_t lookup(const EmbeddingArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Zeroing of table rows [begin, end) by `blocks` workgroups of kIn threads, of which this is number `block`.
+template <class T, int kIn>
+__device__ __forceinline__ void zero_rows(const EmbeddingArgs &a, int64_t begin, int64_t end, int64_t block, int64_t blocks) {
+    const uint32_t per_row = static_cast<uint32_t>((a.cols + 7) / 8);
+    const int64_t n = (end - begin) * per_row;
+    for (int64_t i = block * kIn + threadIdx.x; i < n; i += blocks * kIn) {
+        const int64_t row = n >> 32 ? i / per_row : static_cast<uint32_t>(i) / per_row, col = (i - row * per_row) * 8;
+        store_cols(static_cast<T *>(a.grad_table) + (begin + row) * a.ld_grad_table + col, vec8<T>(T(0.f)),
+                   static_cast<int>(min(a.cols - col, int64_t(8))));
+    }
+}
+
+using f64x8 = vec8<double>;
+
+// Columns col .. col + kW - 1 of table row t from their sums.
+template <class T, int kW>
+__device__ __forceinline__ void write_sums(const EmbeddingArgs &a, int64_t t, int64_t col, const double (&sum)[kW]) {
+    T *to = static_cast<T *>(a.grad_table) + t * a.ld_grad_table + col;
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+        if (col + j < a.cols) to[j] = static_cast<T>(static_cast<float>(sum[j] * a.scale));
+}
+
+// ---- gradient of a small table ----------------------------------------------------------
+
+// A table whose rows fit LDS: a workgroup takes a strip of rows of grad_out in their order, without
+// a sorted list, and adds each to a sum of its index in LDS.  A thread owns four columns, `groups` threads
+// share a column with sums of their own, so no two add to the same place and the order is fixed.  With
+// more than one strip a second kernel adds their sums.
+constexpr int kSmallCols = 4;  // columns of a thread
+struct Strips {
+    int threads;        // of a workgroup
+    int groups, lanes;  // lanes: threads of a row's columns; groups x lanes = threads
+    int slices;         // how often the lanes cover the columns
+    int64_t count, rows;  // strips; rows of one
+    float *part;          // [strip][table row][column]
+};
+
+// The rows of a strip that a thread adds to its sums at `mine`.  kWhole: all its columns are there.
+template <class T, bool kWhole>
+__device__ __forceinline__ void add_strip(const EmbeddingArgs &a, const Strips &s, int64_t strip, int group, int64_t col,
+                                          f32x4 *mine) {
+    using Vec = T __attribute__((ext_vector_type(kSmallCols)));
+    constexpr int kAhead = 16;
+    const int n = kWhole ? kSmallCols : static_cast<int>(a.cols - col);
+    const T *from = static_cast<const T *>(a.grad_out) + col;
+    const int64_t end = min(a.rows, (strip + 1) * s.rows);
+    for (int64_t i = strip * s.rows + group; i < end; i += int64_t(kAhead) * s.groups) {
+        Vec v[kAhead];
+        uint32_t t[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t row = min(i + j * s.groups, end - 1);
+            t[j] = index_at(a, row, kNone);
+            const T *p = from + row * a.ld_grad_out;
+            if (kWhole)
+                __builtin_memcpy(&v[j], p, sizeof(Vec));
+            else
+                v[j] = load_first<Vec>(p, n);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (t[j] != kNone && i + j * s.groups < end) mine[t[j] * s.lanes] += __builtin_convertvector(v[j], f32x4);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_small(EmbeddingArgs a, Strips s) {
+    constexpr int kW = kSmallCols;
+    using Sum = f32x4;
+    extern __shared__ char lds[];
+    Sum *sums = reinterpret_cast<Sum *>(lds);
+    const int tid = threadIdx.x, lane = tid & (s.lanes - 1), group = tid / s.lanes;
+    const int table = static_cast<int>(a.table_rows);
+    const uint32_t strip = blockIdx.x / static_cast<uint32_t>(s.slices), slice = blockIdx.x - strip * s.slices;
+    const int64_t col = (int64_t(slice) * s.lanes + lane) * kW;
+    for (int i = tid; i < table * s.threads; i += s.threads) sums[i] = Sum(0.f);
+    __syncthreads();
+    Sum *mine = sums + group * table * s.lanes + lane;
+    if (col + kW <= a.cols)
+        add_strip<T, true>(a, s, strip, group, col, mine);
+    else if (col < a.cols)
+        add_strip<T, false>(a, s, strip, group, col, mine);
+    __syncthreads();
+    for (int i = tid; i < table * s.lanes; i += s.threads) {
+        const int t = i / s.lanes;
+        const int64_t at = (int64_t(slice) * s.lanes + i - t * s.lanes) * kW;
+        double total[kW] = {};
+        for (int g = 0; g < s.groups; ++g) {
+#pragma unroll
+            for (int k = 0; k < kW; ++k) total[k] += sums[g * table * s.lanes + i][k];
+        }
+        if (s.count == 1) {
+            write_sums<T, kW>(a, t, at, total);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kW; ++k)
+                if (at + k < a.cols) s.part[(int64_t(strip) * table + t) * a.cols + at + k] = static_cast<float>(total[k]);
+        }
+    }
+}
+
+// A workgroup has 16 sums of the table, 64 threads for each.
+constexpr int kJoinThreads = 1024, kJoinSums = 16;
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads) k_join_small(EmbeddingArgs a, Strips s) {
+    constexpr int kShares = kJoinThreads / kJoinSums;
+    __shared__ double sums[kShares][kJoinSums];
+    const int64_t n = a.table_rows * a.cols, at = int64_t(blockIdx.x) * kJoinSums + threadIdx.x % kJoinSums;
+    const int share = threadIdx.x / kJoinSums;
+    double sum[1] = {};
+    if (at < n) {
+#pragma unroll 8
+        for (int64_t i = share; i < s.count; i += kShares) sum[0] += s.part[i * n + at];
+    }
+    sums[share][threadIdx.x % kJoinSums] = sum[0];
+    __syncthreads();
+    if (share || at >= n) return;
+    for (int i = 1; i < kShares; ++i) sum[0] += sums[i][threadIdx.x];
+    const int64_t t = at / a.cols;
+    write_sums<T, 1>(a, t, at - t * a.cols, sum);
+}
+
 // ---- sort -----------------------------------------------------------------------------
 
-// A workgroup sorts tiles of kTile pairs, four a thread: thread t of wave w has the pairs
-// 256 w + 64 j + lane (j = 0..3), so a wave's pairs are consecutive and its ballots rank them in order.
-constexpr int kItems = 4, kTile = kThreads * kItems, kWaves = kThreads / 64, kRadix = 256;
+// A workgroup sorts tiles of pairs, kItems a thread: lane l of wave w has the pairs 64 (kItems w + j) + l
+// (j = 0 .. kItems - 1), so a wave's pairs are consecutive and its ballots rank them in order.
+// The ballots keep a compute unit busy, so tiles are small: sixteen pairs a thread, 16384 in one workgroup,
+// took 45 us for two passes; over 16 workgroups the four kernels take 20.
+constexpr int kItems = 4, kRadix = 256, kTile = kThreads * kItems, kWaves = kThreads / 64;
+// Up to so many pairs one workgroup sorts by itself, all passes in one launch: 8 us for one pass, 11 for two.
+constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / 64, kMostOne = kOneThreads * kItems;
 constexpr int kMostBlocks = 256;  // workgroups of a pass
-constexpr int kOneWaves = 16, kOneTile = 64 * kOneWaves * kItems;  // what one workgroup sorts by itself
-
 struct Sort {
     int64_t rows;
     uint32_t *key[2], *pos[2];  // key and position; the last pass writes [0]
-    uint32_t *count;            // [pass][block][digit]
+    uint32_t *count;            // [block][digit]
     int blocks, tiles;          // of a pass; tiles of a block
-    int passes;
+    int bits, passes;
+    int64_t zero_begin, zero_end;  // table rows that the workgroups past the sorting ones zero
 };
+
+template <class T, int kIn>
+__device__ __forceinline__ void zero_share(const EmbeddingArgs &a, const Sort &s) {
+    zero_rows<T, kIn>(a, s.zero_begin, s.zero_end, int64_t(blockIdx.x) - s.blocks, int64_t(gridDim.x) - s.blocks);
+}
 
 // Lanes of the wave with the same digit (of `bits` bits); those that are not `in` have none.
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool in) {
@@ -118,9 +267,9 @@ __device__ __forceinline__ void rank_in_wave(const uint32_t (&digit)[kItems], co
     }
 }
 
-// Exclusive sums of `n` <= 4 * threads counters in order, in place; every thread takes four.  Returns
-// nothing; `scratch` holds a word a wave.
-template <int kWavesIn>
+// Exclusive sums of `n` counters, at most four a thread, in order and in place; `scratch` holds a word for
+// each of the kIn waves.
+template <int kIn>
 __device__ __forceinline__ void exclusive_sums(uint32_t *v, int n, uint32_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 63;
     uint32_t mine[4], sum = 0;
@@ -138,7 +287,8 @@ __device__ __forceinline__ void exclusive_sums(uint32_t *v, int n, uint32_t *scr
     if (lane == 63) scratch[tid >> 6] = scan;
     __syncthreads();
     uint32_t run = scan - sum;
-    for (int w = 0; w < (tid >> 6); ++w) run += scratch[w];
+#pragma unroll
+    for (int w = 0; w < kIn; ++w) run += w < (tid >> 6) ? scratch[w] : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (4 * tid + j < n) v[4 * tid + j] = run;
@@ -147,14 +297,17 @@ __device__ __forceinline__ void exclusive_sums(uint32_t *v, int n, uint32_t *scr
     __syncthreads();
 }
 
-// Bits of pass p of `passes` over keys of `bits` bits, shared out evenly.
-__device__ __forceinline__ int pass_shift(int bits, int passes, int p) { return bits * p / passes; }
+// The first bit of pass p: the keys' bits are shared out evenly, at most eight a pass.
+__device__ __forceinline__ int pass_shift(const Sort &s, int p) { return s.bits * p / s.passes; }
 
-// All passes by one workgroup of kOneWaves waves, in LDS.
-__global__ void __launch_bounds__(64 * kOneWaves) k_sort_one(EmbeddingArgs a, Sort s, int bits) {
-    __shared__ uint32_t keys[kOneTile], counts[kRadix * kOneWaves], scratch[kOneWaves];
-    __shared__ uint16_t at[kOneTile];
+// All passes by one workgroup, in LDS, over at most kMostOne pairs.
+template <class T>
+__global__ void __launch_bounds__(kOneThreads) k_sort_one(EmbeddingArgs a, Sort s) {
+    if (blockIdx.x) return zero_share<T, kOneThreads>(a, s);
+    __shared__ uint32_t keys[kMostOne], counts[kRadix * kOneWaves], scratch[kOneWaves];
+    __shared__ uint16_t at[kMostOne];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = static_cast<int>(s.rows);
+    if (n == 0) return;
     uint32_t key[kItems], pos[kItems], rank[kItems], digit[kItems];
     bool in[kItems];
 #pragma unroll
@@ -162,11 +315,12 @@ __global__ void __launch_bounds__(64 * kOneWaves) k_sort_one(EmbeddingArgs a, So
         const int i = 64 * (kItems * wave + j) + lane;
         in[j] = i < n;
         pos[j] = i;
-        key[j] = in[j] ? static_cast<uint32_t>(index_at(a, i, a.table_rows)) : 0;
+        key[j] = index_at(a, min(i, n - 1), static_cast<uint32_t>(a.table_rows));
     }
     for (int p = 0; p < s.passes; ++p) {
-        const int shift = pass_shift(bits, s.passes, p), width = pass_shift(bits, s.passes, p + 1) - shift;
-        for (int i = tid; i < kRadix * kOneWaves; i += 64 * kOneWaves) counts[i] = 0;
+        const int shift = pass_shift(s, p), width = pass_shift(s, p + 1) - shift;
+#pragma unroll
+        for (int j = 0; j < kRadix * kOneWaves / kOneThreads; ++j) counts[j * kOneThreads + tid] = 0;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kItems; ++j) digit[j] = key[j] >> shift & ((1u << width) - 1);
@@ -193,58 +347,61 @@ __global__ void __launch_bounds__(64 * kOneWaves) k_sort_one(EmbeddingArgs a, So
                 at[to] = static_cast<uint16_t>(pos[j]);
             }
         }
+        if (last) return;
         __syncthreads();
-        if (!last) {
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                const int i = 64 * (kItems * wave + j) + lane;
-                if (in[j]) key[j] = keys[i], pos[j] = at[i];
-            }
+        for (int j = 0; j < kItems; ++j) {
+            const int i = 64 * (kItems * wave + j) + lane;
+            if (in[j]) key[j] = keys[i], pos[j] = at[i];
         }
     }
 }
 
-// The first pass's counts of each workgroup's digits; the later passes' are zeroed.
-__global__ void __launch_bounds__(kThreads) k_count(EmbeddingArgs a, Sort s, int bits) {
+// Key i of a pass: of the index itself in the first, else of what the pass before wrote.
+template <bool kFirst>
+__device__ __forceinline__ uint32_t key_at(const EmbeddingArgs &a, const Sort &s, int pass, int64_t i) {
+    return kFirst ? index_at(a, i, static_cast<uint32_t>(a.table_rows)) : s.key[(s.passes - pass) & 1][i];
+}
+
+// Counts of each workgroup's digits of a pass.
+template <class T, bool kFirst>
+__global__ void __launch_bounds__(kThreads) k_count(EmbeddingArgs a, Sort s, int pass) {
+    if (static_cast<int>(blockIdx.x) >= s.blocks) return zero_share<T, kThreads>(a, s);
     __shared__ uint32_t counts[kRadix];
-    const int tid = threadIdx.x, width = pass_shift(bits, s.passes, 1);
+    const int tid = threadIdx.x, shift = pass_shift(s, pass), width = pass_shift(s, pass + 1) - shift;
     counts[tid] = 0;
     __syncthreads();
     const int64_t first = int64_t(blockIdx.x) * s.tiles * kTile, end = min(s.rows, first + int64_t(s.tiles) * kTile);
+#pragma unroll 4
     for (int64_t i = first + tid; i < end; i += kThreads)
-        atomicAdd(&counts[static_cast<uint32_t>(index_at(a, i, a.table_rows)) & ((1u << width) - 1)], 1u);
+        atomicAdd(&counts[key_at<kFirst>(a, s, pass, i) >> shift & ((1u << width) - 1)], 1u);
     __syncthreads();
     s.count[blockIdx.x * kRadix + tid] = counts[tid];
-    for (int p = 1; p < s.passes; ++p) s.count[(int64_t(p) * s.blocks + blockIdx.x) * kRadix + tid] = 0;
 }
 
 // One pass: every pair to its place.  The place of a workgroup's first pair of a digit is the number of
 // pairs of smaller digits and of those of the digit in the workgroups before it, from the counts.
-// Each pair also counts for the next pass, in the workgroup that will have it (integer sums: exact in
-// any order).
-__global__ void __launch_bounds__(kThreads) k_place(EmbeddingArgs a, Sort s, int bits, int pass) {
+template <class T, bool kFirst>
+__global__ void __launch_bounds__(kThreads) k_place(EmbeddingArgs a, Sort s, int pass) {
+    if (static_cast<int>(blockIdx.x) >= s.blocks) return zero_share<T, kThreads>(a, s);
     __shared__ uint32_t total[kRadix], mine[kRadix], counts[kWaves * kRadix], scratch[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int shift = pass_shift(bits, s.passes, pass), width = pass_shift(bits, s.passes, pass + 1) - shift;
-    const int next = pass + 1 < s.passes ? pass_shift(bits, s.passes, pass + 1) : 0;
-    const int next_width = next ? pass_shift(bits, s.passes, pass + 2) - next : 0;
-    const bool from_index = pass == 0;
-    // the last pass writes [0], each one before it the other buffer
-    const int to_buffer = (s.passes - 1 - pass) & 1;
-    const uint32_t *key_in = s.key[to_buffer ^ 1], *pos_in = s.pos[to_buffer ^ 1];
+    const int shift = pass_shift(s, pass), width = pass_shift(s, pass + 1) - shift;
+    const uint32_t digits = 1u << width;
+    const int to_buffer = (s.passes - 1 - pass) & 1;  // the last pass writes [0]
+    const uint32_t *pos_in = s.pos[to_buffer ^ 1];
     uint32_t *key_out = s.key[to_buffer], *pos_out = s.pos[to_buffer];
 
-    // 2^width digits by 256 >> width threads each, which share the workgroups
-    total[tid] = 0;
-    mine[tid] = 0;
+    total[tid] = 0, mine[tid] = 0;
     __syncthreads();
-    const uint32_t *count = s.count + int64_t(pass) * s.blocks * kRadix;
     {
-        const int digit = tid & ((1 << width) - 1), step = kThreads >> width;
+        // a digit by kThreads / digits threads, which share the workgroups
+        const uint32_t digit = tid & (digits - 1);
+        const int step = kThreads >> width;
         uint32_t all = 0, before = 0;
 #pragma unroll 8
         for (int b = tid >> width; b < s.blocks; b += step) {
-            const uint32_t c = count[b * kRadix + digit];
+            const uint32_t c = s.count[b * kRadix + digit];
             all += c;
             before += b < static_cast<int>(blockIdx.x) ? c : 0;
         }
@@ -254,7 +411,6 @@ __global__ void __launch_bounds__(kThreads) k_place(EmbeddingArgs a, Sort s, int
     __syncthreads();
     exclusive_sums<kWaves>(total, kRadix, scratch);
     mine[tid] += total[tid];
-    __syncthreads();
 
     for (int tile = 0; tile < s.tiles; ++tile) {
         const int64_t first = (int64_t(blockIdx.x) * s.tiles + tile) * kTile;
@@ -265,30 +421,26 @@ __global__ void __launch_bounds__(kThreads) k_place(EmbeddingArgs a, Sort s, int
         for (int j = 0; j < kItems; ++j) {
             const int64_t i = first + 64 * (kItems * wave + j) + lane;
             in[j] = i < s.rows;
-            key[j] = 0, pos[j] = 0;
-            if (in[j] && from_index) {
-                key[j] = static_cast<uint32_t>(index_at(a, i, a.table_rows));
-                pos[j] = static_cast<uint32_t>(i);
-            } else if (in[j]) {
-                key[j] = key_in[i];
-                pos[j] = pos_in[i];
-            }
-            digit[j] = key[j] >> shift & ((1u << width) - 1);
+            key[j] = key_at<kFirst>(a, s, pass, min(i, s.rows - 1));
+            pos[j] = kFirst ? static_cast<uint32_t>(i) : pos_in[min(i, s.rows - 1)];
+            digit[j] = key[j] >> shift & (digits - 1);
         }
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) counts[w * kRadix + tid] = 0;
+        for (int j = 0; j < kWaves * kRadix / kThreads; ++j) counts[j * kThreads + tid] = 0;
         __syncthreads();
         rank_in_wave(digit, in, width, counts + wave * kRadix, rank);
         __syncthreads();
         // thread = digit: where each wave's pairs of it begin, and the next tile's
-        uint32_t run = mine[tid];
+        {
+            uint32_t run = mine[tid];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const uint32_t c = counts[w * kRadix + tid];
-            counts[w * kRadix + tid] = run;
-            run += c;
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t c = counts[w * kRadix + tid];
+                counts[w * kRadix + tid] = run;
+                run += c;
+            }
+            mine[tid] = run;
         }
-        mine[tid] = run;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {
@@ -296,18 +448,12 @@ __global__ void __launch_bounds__(kThreads) k_place(EmbeddingArgs a, Sort s, int
             const uint32_t to = counts[wave * kRadix + digit[j]] + rank[j];
             key_out[to] = key[j];
             pos_out[to] = pos[j];
-            if (next_width) {
-                const uint32_t block = to / static_cast<uint32_t>(s.tiles * kTile);
-                atomicAdd(&s.count[(int64_t(pass + 1) * s.blocks + block) * kRadix +
-                                   (key[j] >> next & ((1u << next_width) - 1))],
-                          1u);
-            }
         }
         __syncthreads();
     }
 }
 
-// ---- sums -----------------------------------------------------------------------------
+// ---- sums of sorted rows ------------------------------------------------------------------
 
 struct Chunks {
     const uint32_t *key, *pos;
@@ -316,11 +462,8 @@ struct Chunks {
     int64_t count;
     int length;
     int lanes, slices;  // lanes of a row's columns, and how often they cover them
-    int64_t blocks;     // workgroups that sum; the others zero table rows
-    int fill_rows;      // table rows of one of those
+    int64_t blocks;
 };
-
-using f64x8 = vec8<double>;
 
 template <class T>
 __device__ __forceinline__ void write_row(const EmbeddingArgs &a, uint32_t t, int64_t col, f64x8 sum, int n) {
@@ -329,74 +472,49 @@ __device__ __forceinline__ void write_row(const EmbeddingArgs &a, uint32_t t, in
                from_f32<T>(__builtin_convertvector(sum, f32x8)), n);
 }
 
-// The number of sorted keys below t.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t *key, int64_t n, uint32_t t) {
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (key[mid] < t)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-template <class T>
-__device__ __forceinline__ void zero_absent(const EmbeddingArgs &a, const Chunks &c, int64_t first) {
-    __shared__ uint32_t absent[kThreads / 32];
-    const int n = static_cast<int>(min<int64_t>(c.fill_rows, a.table_rows - first));
-    if (threadIdx.x < kThreads / 32) absent[threadIdx.x] = 0;
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) < n) {
-        const uint32_t t = static_cast<uint32_t>(first + threadIdx.x);
-        const int64_t at = lower_bound(c.key, c.rows, t);
-        if (at == c.rows || c.key[at] != t) atomicOr(&absent[threadIdx.x >> 5], 1u << (threadIdx.x & 31));
-    }
-    __syncthreads();
-    const int per_row = static_cast<int>((a.cols + 7) / 8);
-    for (int r = 0; r < n; ++r) {
-        if (!(absent[r >> 5] >> (r & 31) & 1)) continue;
-        T *row = static_cast<T *>(a.grad_table) + (first + r) * a.ld_grad_table;
-        for (int i = threadIdx.x; i < per_row; i += kThreads)
-            store_cols(row + 8 * int64_t(i), vec8<T>(T(0.f)), static_cast<int>(min<int64_t>(a.cols - 8 * int64_t(i), 8)));
-    }
-}
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_sums(EmbeddingArgs a, Chunks c) {
-    if (blockIdx.x >= c.blocks) return zero_absent<T>(a, c, (int64_t(blockIdx.x) - c.blocks) * c.fill_rows);
-    const int64_t item = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / c.lanes, chunk = item / c.slices;
-    const int64_t col = ((item - chunk * c.slices) * c.lanes + threadIdx.x % c.lanes) * 8;
-    if (chunk >= c.count || col >= a.cols) return;
-    const int n = static_cast<int>(min<int64_t>(a.cols - col, 8));
+// kWhole: all eight columns are there.
+template <class T, bool kWhole>
+__device__ __forceinline__ void walk_chunk(const EmbeddingArgs &a, const Chunks &c, int64_t chunk, int64_t col) {
+    const int n = kWhole ? 8 : static_cast<int>(a.cols - col);
     const int64_t begin = chunk * c.length, end = min(c.rows, begin + c.length);
     const T *from = static_cast<const T *>(a.grad_out) + col;
     float *part = c.part + chunk * 2 * c.lanes * c.slices * 8 + col;
 
-    uint32_t run = c.key[begin];
-    bool head = begin > 0 && c.key[begin - 1] == run;  // whether the run began in an earlier chunk
-    f64x8 sum = {};
     constexpr int kAhead = 8;
-    for (int64_t i = begin; i < end && run < a.table_rows; i += kAhead) {
-        uint32_t key[kAhead];
-        vec8<T> v[kAhead];
+    uint32_t key[kAhead], pos[kAhead];
+    const auto fetch = [&](int64_t i) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t at = min(i + j, end - 1);
-            key[j] = i + j < end ? c.key[at] : run;
-            v[j] = load_cols(from + int64_t(c.pos[at]) * a.ld_grad_out, n);
+            key[j] = c.key[at];
+            pos[j] = c.pos[at];
         }
+    };
+    fetch(begin);
+    const uint32_t before = c.key[begin ? begin - 1 : 0], after = c.key[min(end, c.rows - 1)];
+    uint32_t run = key[0];
+    bool head = begin > 0 && before == run;  // whether the run began in an earlier chunk
+    f64x8 sum = {};
+    for (int64_t i = begin; i < end && run < a.table_rows; i += kAhead) {
+        uint32_t now[kAhead];
+        vec8<T> v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            now[j] = key[j];
+            const T *p = from + int64_t(pos[j]) * a.ld_grad_out;
+            v[j] = kWhole ? load8(p) : load_first<vec8<T>>(p, n);
+        }
+        fetch(min(i + kAhead, end - 1));
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             if (i + j >= end) break;
-            if (key[j] != run) {
+            if (now[j] != run) {
                 if (head)
                     store8(part, __builtin_convertvector(sum, f32x8));
                 else
                     write_row<T>(a, run, col, sum, n);
                 head = false;
-                run = key[j];
+                run = now[j];
                 sum = f64x8{};
                 if (run >= a.table_rows) break;
             }
@@ -404,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) k_sums(EmbeddingArgs a, Chunks c) {
         }
     }
     if (run >= a.table_rows) return;  // from here on the list holds pairs of no table row
-    const bool on = end < c.rows && c.key[end] == run;
+    const bool on = end < c.rows && after == run;
     if (head)
         store8(part, __builtin_convertvector(sum, f32x8));
     else if (on)
@@ -413,59 +531,116 @@ __global__ void __launch_bounds__(kThreads) k_sums(EmbeddingArgs a, Chunks c) {
         write_row<T>(a, run, col, sum, n);
 }
 
-// A workgroup for each chunk whose last run goes on in the next: the sum of what the chunks hold of it.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_sums(EmbeddingArgs a, Chunks c) {
+    const int64_t item = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / c.lanes, chunk = item / c.slices;
+    const int64_t col = ((item - chunk * c.slices) * c.lanes + threadIdx.x % c.lanes) * 8;
+    if (chunk >= c.count || col >= a.cols) return;
+    if (col + 8 <= a.cols)
+        walk_chunk<T, true>(a, c, chunk, col);
+    else
+        walk_chunk<T, false>(a, c, chunk, col);
+}
+
+// The last chunk that a run reaches, which begins in `chunk` and reaches the next: the wave's 64 lanes probe
+// the chunks' first keys, near ones first.
+__device__ __forceinline__ int64_t last_chunk(const Chunks &c, int64_t chunk, uint32_t run) {
+    const int lane = threadIdx.x & 63;
+    int64_t lo = chunk + 1, step = 1;  // lo: reached
+    for (;;) {
+        const int64_t i = lo + step * (lane + 1);
+        const bool reached = i < c.count && c.key[i * c.length] == run;
+        const int n = __popcll(__ballot(reached));
+        lo += step * n;
+        if (n == 64) {
+            step *= 64;
+        } else {
+            if (step == 1) return lo;
+            step /= 64;
+        }
+    }
+}
+
+// A workgroup for each chunk whose last run goes on in the next and kJoinCols columns (blockIdx.y): the sum of
+// what the chunks hold of it.
+constexpr int kJoinLanes = 32, kJoinCols = kJoinLanes * 8;
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_join_runs(EmbeddingArgs a, Chunks c) {
-    constexpr int kLanes = 32, kGroups = kThreads / kLanes;
-    __shared__ double sums[kGroups][kLanes * 8];
+    constexpr int kGroups = kThreads / kJoinLanes;
+    __shared__ double sums[kGroups][kJoinCols];
     const int64_t chunk = blockIdx.x, begin = chunk * c.length, end = begin + c.length;  // not the last chunk
-    const uint32_t run = c.key[end - 1];
-    if (run >= a.table_rows || c.key[end] != run) return;
-    if (begin > 0 && c.key[begin - 1] == run) return;  // it began before this chunk
-    const int64_t stop = lower_bound(c.key, c.rows, run + 1), last = (stop - 1) / c.length;
-    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int64_t row = int64_t(c.lanes) * c.slices * 8;
-    for (int64_t col0 = 0; col0 < a.cols; col0 += kLanes * 8) {
-        const int64_t col = col0 + lane * 8;
-        f64x8 sum = {};
-        if (col < a.cols) {
-            if (group == 0) sum = __builtin_convertvector(load8(c.part + (chunk * 2 + 1) * row + col), f64x8);
-#pragma unroll 4
-            for (int64_t i = chunk + 1 + group; i <= last; i += kGroups)
-                sum += __builtin_convertvector(load8(c.part + i * 2 * row + col), f64x8);
-        }
+    const uint32_t before = c.key[begin ? begin - 1 : 0], run = c.key[end - 1], after = c.key[end];
+    if (run >= a.table_rows || after != run) return;
+    if (begin > 0 && before == run) return;  // it began before this chunk
+    const int64_t last = last_chunk(c, chunk, run);
+    const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
+    const int64_t row = int64_t(c.lanes) * c.slices * 8, col = int64_t(blockIdx.y) * kJoinCols + lane * 8;
+    f64x8 sum = {};
+    if (col < a.cols) {
+        if (group == 0) sum = __builtin_convertvector(load8(c.part + (chunk * 2 + 1) * row + col), f64x8);
+        for (int64_t i = chunk + 1 + group; i <= last; i += 8 * kGroups) {
+            f32x8 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[group][lane * 8 + j] = sum[j];
-        __syncthreads();
-        if (group == 0 && col < a.cols) {
-            for (int g = 1; g < kGroups; ++g) {
+            for (int j = 0; j < 8; ++j) v[j] = load8(c.part + min(i + j * kGroups, last) * 2 * row + col);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += sums[g][lane * 8 + j];
-            }
-            write_row<T>(a, run, col, sum, static_cast<int>(min<int64_t>(a.cols - col, 8)));
+            for (int j = 0; j < 8; ++j)
+                if (i + j * kGroups <= last) sum += __builtin_convertvector(v[j], f64x8);
         }
-        __syncthreads();
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[group][lane * 8 + j] = sum[j];
+    __syncthreads();
+    if (group || col >= a.cols) return;
+    for (int g = 1; g < kGroups; ++g) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += sums[g][lane * 8 + j];
+    }
+    write_row<T>(a, run, col, sum, static_cast<int>(min<int64_t>(a.cols - col, 8)));
 }
 
 // ---- launches -------------------------------------------------------------------------
 
 constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
+// Whether the table is summed in LDS.  At 17 to 32 rows a workgroup has 128 threads of sums, and wide rows
+// are better sorted (a replayed graph with the gradient, us, sorted and here; about 18 of it are the replay's):
+// 10 rows, 280000 x 256 bf16: 88 and 43; 10, 5000 x 512: 26 and 19; 32, 280000 x 256: 73 and 70; 32, 5000 x 512:
+// 26 and 39; 32, 5000 x 128 fp32: 25 and 19; 64, 5000 x 128: 25 and 29.
+bool small_table(int64_t table_rows, int64_t cols) { return table_rows <= 16 || (table_rows <= 32 && cols <= 256); }
+
 struct Plan {
+    bool small;  // see small_table
+    Strips strips;
     bool one;  // one workgroup sorts
     int bits, passes, blocks, tiles;
     Chunks chunks;
-    int64_t fill_blocks;
     size_t list, count, part, bytes;  // bytes of one list of keys or positions, of the counts and partial sums
 };
 
 Plan plan_of(int64_t table_rows, int64_t cols, int64_t rows) {
     Plan p{};
+    p.small = small_table(table_rows, cols);
+    if (p.small) {
+        Strips &s = p.strips;
+        s.threads = table_rows <= 16 ? kThreads : kThreads / 2;  // 64 KB of sums at most
+        const int64_t pieces = std::max<int64_t>((cols + kSmallCols - 1) / kSmallCols, 1);
+        for (s.lanes = 1; s.lanes < s.threads && s.lanes < pieces; s.lanes *= 2) {
+        }
+        s.groups = s.threads / s.lanes;
+        s.slices = static_cast<int>((pieces + s.lanes - 1) / s.lanes);
+        // two workgroups a compute unit, 16 rows a thread at least and 4096 at most (fp32 sums)
+        const int64_t least = (rows + int64_t(s.groups) * 4096 - 1) / (int64_t(s.groups) * 4096);
+        const int64_t most = (rows + s.groups * 16 - 1) / (s.groups * 16);
+        s.count = std::max<int64_t>(1, std::max(least, std::min<int64_t>(most, std::max(1, 512 / s.slices))));
+        s.rows = (rows + s.count - 1) / s.count;
+        p.part = s.count > 1 ? up(static_cast<size_t>(s.count) * table_rows * cols * 4) : 0;
+        p.bytes = p.part;
+        return p;
+    }
     for (p.bits = 1; p.bits < 32 && (table_rows >> p.bits); ++p.bits) {
     }
     p.passes = (p.bits + 7) / 8;
-    p.one = rows <= kOneTile;
+    p.one = rows <= kMostOne;
     const int64_t tiles = (rows + kTile - 1) / kTile;
     p.tiles = static_cast<int>((tiles + kMostBlocks - 1) / kMostBlocks);
     p.blocks = p.tiles ? static_cast<int>((tiles + p.tiles - 1) / p.tiles) : 0;
@@ -479,10 +654,8 @@ Plan plan_of(int64_t table_rows, int64_t cols, int64_t rows) {
     c.length = static_cast<int>(std::max<int64_t>(16, (rows + 8191) / 8192 + 7)) / 8 * 8;
     c.count = (rows + c.length - 1) / c.length;
     c.blocks = (c.count * c.slices * c.lanes + kThreads - 1) / kThreads;
-    c.fill_rows = static_cast<int>(std::min<int64_t>(kThreads, std::max<int64_t>(1, 32768 / (pieces * 16))));
-    p.fill_blocks = (table_rows + c.fill_rows - 1) / c.fill_rows;
     p.list = up(static_cast<size_t>(rows) * 4);
-    p.count = p.one ? 0 : up(static_cast<size_t>(p.passes) * p.blocks * kRadix * 4);
+    p.count = !p.one ? up(static_cast<size_t>(p.blocks) * kRadix * 4) : 0;
     p.part = c.count > 1 ? up(static_cast<size_t>(c.count) * 2 * c.lanes * c.slices * 8 * 4) : 0;
     p.bytes = p.list * (p.one || p.passes == 1 ? 2 : 4) + p.count + p.part;
     return p;
@@ -492,13 +665,23 @@ template <class T>
 hipError_t gradient(const EmbeddingArgs &a, hipStream_t stream) {
     Plan p = plan_of(a.table_rows, a.cols, a.rows);
     char *ws = static_cast<char *>(a.workspace);
+    if (p.small) {
+        p.strips.part = reinterpret_cast<float *>(ws);
+        const unsigned bytes = static_cast<unsigned>(a.table_rows * p.strips.threads * kSmallCols * 4);
+        const dim3 blocks(static_cast<unsigned>(p.strips.count * p.strips.slices));
+        k_small<T><<<blocks, dim3(p.strips.threads), bytes, stream>>>(a, p.strips);
+        const int64_t joins = (a.table_rows * a.cols + kJoinSums - 1) / kJoinSums;
+        if (p.strips.count > 1)
+            k_join_small<T><<<dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, stream>>>(a, p.strips);
+        return hipGetLastError();
+    }
     const auto take = [&](size_t bytes) {
         char *at = ws;
         ws += bytes;
         return reinterpret_cast<uint32_t *>(at);
     };
     Sort s{};
-    s.rows = a.rows, s.blocks = p.blocks, s.tiles = p.tiles, s.passes = p.passes;
+    s.rows = a.rows, s.blocks = p.blocks, s.tiles = p.tiles, s.bits = p.bits, s.passes = p.passes;
     s.key[0] = take(p.list);
     s.pos[0] = take(p.list);
     if (!p.one && p.passes > 1) {
@@ -509,15 +692,34 @@ hipError_t gradient(const EmbeddingArgs &a, hipStream_t stream) {
     Chunks &c = p.chunks;
     c.part = reinterpret_cast<float *>(take(p.part));
     c.key = s.key[0], c.pos = s.pos[0];
-    if (a.rows && p.one) {
-        k_sort_one<<<dim3(1), dim3(64 * kOneWaves), 0, stream>>>(a, s, p.bits);
-    } else if (a.rows) {
-        const dim3 blocks(static_cast<unsigned>(p.blocks)), threads(kThreads);
-        k_count<<<blocks, threads, 0, stream>>>(a, s, p.bits);
-        for (int pass = 0; pass < p.passes; ++pass) k_place<<<blocks, threads, 0, stream>>>(a, s, p.bits, pass);
+    // The sort waits for memory more than it uses it, so its launches zero the table between them; the
+    // sums then write the rows that are used.
+    using Zero = typename std::conditional<sizeof(T) == 4, float, f16>::type;  // of T's size
+    const int turns = p.one ? 1 : 2 * s.passes;
+    const int64_t zeros = (a.table_rows / turns + 1) * ((a.cols + 7) / 8);
+    s.blocks = p.one ? 1 : s.blocks;
+    const dim3 threads(p.one ? kOneThreads : kThreads);
+    const dim3 grid(static_cast<unsigned>(s.blocks + std::min<int64_t>((zeros + 4 * threads.x - 1) / (4 * threads.x), 2048)));
+    for (int turn = 0; turn < turns; ++turn) {
+        s.zero_begin = a.table_rows * turn / turns;
+        s.zero_end = a.table_rows * (turn + 1) / turns;
+        const auto run = [&](auto first) {
+            constexpr bool kFirst = decltype(first)::value;
+            if (turn % 2 == 0)
+                k_count<Zero, kFirst><<<grid, threads, 0, stream>>>(a, s, turn / 2);
+            else
+                k_place<Zero, kFirst><<<grid, threads, 0, stream>>>(a, s, turn / 2);
+        };
+        if (p.one)
+            k_sort_one<Zero><<<grid, threads, 0, stream>>>(a, s);
+        else if (turn < 2)
+            run(std::true_type());
+        else
+            run(std::false_type());
     }
-    k_sums<T><<<dim3(static_cast<unsigned>(c.blocks + p.fill_blocks)), dim3(kThreads), 0, stream>>>(a, c);
-    if (c.count > 1) k_join_runs<T><<<dim3(static_cast<unsigned>(c.count - 1)), dim3(kThreads), 0, stream>>>(a, c);
+    if (c.count) k_sums<T><<<dim3(static_cast<unsigned>(c.blocks)), dim3(kThreads), 0, stream>>>(a, c);
+    if (c.count > 1) k_join_runs<T><<<dim3(static_cast<unsigned>(c.count - 1), static_cast<unsigned>((a.cols + kJoinCols - 1) / kJoinCols)),
+                         dim3(kThreads), 0, stream>>>(a, c);
     return hipGetLastError();
 }
 
@@ -527,7 +729,9 @@ size_t embedding_workspace(int64_t table_rows, int64_t cols, int64_t rows) { ret
 
 int64_t embedding_blocks(int64_t table_rows, int64_t cols, int64_t rows) {
     const Plan p = plan_of(table_rows, cols, rows);
-    return p.chunks.blocks + p.fill_blocks;
+    const int64_t joins = p.small ? (table_rows * cols + kJoinSums - 1) / kJoinSums * (kJoinThreads / kThreads)
+                                  : p.chunks.count * ((cols + kJoinCols - 1) / kJoinCols);
+    return std::max({p.chunks.blocks, joins, p.strips.count * p.strips.slices});
 }
 
 hipError_t embedding_fwd(oeq_dtype dtype, const EmbeddingArgs &a, hipStream_t stream) {

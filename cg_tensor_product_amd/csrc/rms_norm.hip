@@ -27,7 +27,14 @@ template <class T, int kGroup, int kPieces>
 struct Row {
     vec8<T> v[kPieces];
     static __device__ __forceinline__ int col(int i) { return (i * kGroup + int(threadIdx.x) % kGroup) * 8; }
+    // Where all pieces are whole, as in most rows, the loads are in a row: a value that came by two ways
+    // would be waited for where they meet, before the next load.
     __device__ __forceinline__ void load(const T *row, int cols) {
+        if (cols >= kGroup * kPieces * 8) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) v[i] = load8(row + col(i));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int c = col(i), n = cols - c;
@@ -221,14 +228,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_grad(RmsNormArgs a, float *pa
     }
 }
 
-// grad_weight from the partial sums of `strips` strips: 32 columns a workgroup, eight threads for each.
-__global__ void __launch_bounds__(kThreads) k_join_strips(const float *part, int strips, int cols, float *grad_weight) {
-    constexpr int kCols = 32, kShares = kThreads / kCols;
-    __shared__ double sums[kShares][kCols];
-    const int lane = threadIdx.x % kCols, share = threadIdx.x / kCols, c = blockIdx.x * kCols + lane;
+// grad_weight from the partial sums of `strips` strips: 16 columns a workgroup, 64 threads for each.
+constexpr int kJoinThreads = 1024, kJoinCols = 16;
+__global__ void __launch_bounds__(kJoinThreads) k_join_strips(const float *part, int strips, int cols, float *grad_weight) {
+    constexpr int kShares = kJoinThreads / kJoinCols;
+    __shared__ double sums[kShares][kJoinCols];
+    const int lane = threadIdx.x % kJoinCols, share = threadIdx.x / kJoinCols, c = blockIdx.x * kJoinCols + lane;
     double s = 0.;
     if (c < cols) {
-#pragma unroll 8
+#pragma unroll 16
         for (int i = share; i < strips; i += kShares) s += part[int64_t(i) * cols + c];
     }
     sums[share][lane] = s;
@@ -291,8 +299,8 @@ hipError_t backward(const RmsNormArgs &a, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     if (a.grad_weight)
-        k_join_strips<<<dim3((a.cols + 31) / 32), dim3(kThreads), 0, stream>>>(part, static_cast<int>(strips), a.cols,
-                                                                           a.grad_weight);
+        k_join_strips<<<dim3((a.cols + kJoinCols - 1) / kJoinCols), dim3(kJoinThreads), 0, stream>>>(
+            part, static_cast<int>(strips), a.cols, a.grad_weight);
     return hipGetLastError();
 }
 

@@ -20,7 +20,7 @@ def _emb(dtype=0, table=5, cols=8, rows=4, t=A, ld_t=8, index=A, size=8, scale=1
     return oeq.lib().oeq_embedding_fwd(dtype, table, cols, rows, t, ld_t, index, size, scale, out, ld_o, None)
 
 
-def _emb_bwd(dtype=0, table=5, cols=8, rows=4, index=A, size=8, scale=1.0, go=A, ld_go=8, gt=A, ld_gt=8, ws=A,
+def _emb_bwd(dtype=0, table=50, cols=8, rows=4, index=A, size=8, scale=1.0, go=A, ld_go=8, gt=A, ld_gt=8, ws=A,
              wsb=1 << 20):
     return oeq.lib().oeq_embedding_bwd(dtype, table, cols, rows, index, size, scale, go, ld_go, gt, ld_gt, ws, wsb, None)
 
@@ -62,7 +62,10 @@ def test_embedding_workspace_sizes():
     assert size(0, 1 << 20, 64, 10**6, ctypes.byref(b)) == 0 and b.value >= 4 * 10**6 * 4
     assert size(0, 0, 64, 10, ctypes.byref(b)) == 0 and b.value == 0
     assert size(0, 100, 64, 10, None) == 0
-    assert size(0, 2**31 - 2, 2**31 - 2, 10, ctypes.byref(b)) == 2  # a launch of too many workgroups
+    # a table of few rows: sums of strips of rows, none where one strip holds them all
+    assert size(0, 5, 64, 10, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(0, 5, 64, 10**6, ctypes.byref(b)) == 0 and b.value >= 2 * 5 * 64 * 4
+    assert size(0, 16, 2**31 - 2, 10, ctypes.byref(b)) == 2  # a launch of too many workgroups
 
 
 # ---- rms norm -------------------------------------------------------------------------------

@@ -26,11 +26,22 @@ CASES = {
     "all_absent": (6, 16, 40, 1.0, 1.0),
     "one_row_table": (1, 40, 1000, 1.0, 0.0),
     "one_sorting_group": (700, 72, 4096, 2.0, 0.05),
-    "past_one_group": (255, 33, 4097, 1.0, 0.05),
+    "past_four_a_thread": (255, 33, 4097, 1.0, 0.05),
+    "most_of_one_group": (3000, 16, 16384, 2.0, 0.05),
+    "past_one_group": (255, 33, 16385, 1.0, 0.05),
+    "past_one_group_two_digits": (256, 9, 20000, 1.0, 0.05),
     "two_digits": (256, 8, 5000, 3.0, 0.0),
     "vocabulary": (32000, 520, 6000, 4.0, 0.05),
     "three_digits": (100000, 5, 9000, 3.0, 0.0),
     "few_common": (10, 256, 30000, 1.5, 0.0),
+    "most_of_a_small_table": (16, 100, 2000, 1.0, 0.1),
+    "next_small_table": (17, 100, 2000, 1.0, 0.1),
+    "last_small_table": (32, 256, 900, 1.0, 0.1),
+    "past_a_small_table": (33, 100, 2000, 1.0, 0.1),
+    "small_table_of_wide_rows": (20, 264, 500, 1.0, 0.1),
+    "small_table_wide": (6, 1100, 700, 2.0, 0.05),
+    "counted_passes": (40, 16, 300000, 2.0, 0.01),
+    "counted_two_digits": (1000, 8, 70000, 3.0, 0.01),
     "long": (3, 16, 300000, 1.0, 0.01),
     "wide": (50, 2051, 333, 1.0, 0.0),
 }
@@ -167,8 +178,9 @@ def test_in_the_callers_workspace(name):
     got = oeq.oeq_embedding_bwd(index, g, table.shape[0], workspace=whole[:n])
     assert torch.equal(got, oeq.oeq_embedding_bwd(index, g, table.shape[0]))
     assert torch.all(whole[n:] == 0x5A)
-    with pytest.raises(oeq.OeqError):
-        oeq.oeq_embedding_bwd(index, g, table.shape[0], workspace=whole[:n - 256])
+    if n:
+        with pytest.raises(oeq.OeqError):
+            oeq.oeq_embedding_bwd(index, g, table.shape[0], workspace=whole[:n - 256])
 
 
 def test_a_table_past_32_bit_offsets():
