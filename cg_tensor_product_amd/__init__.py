@@ -40,7 +40,8 @@ EXPORTED = ["oeq_plan_create", "oeq_plan_create_cached", "oeq_plan_destroy", "oe
             "oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
             "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd",
             "oeq_embedding_fwd", "oeq_embedding_workspace_size", "oeq_embedding_bwd", "oeq_rms_norm_workspace_size",
-            "oeq_rms_norm_fwd", "oeq_rms_norm_bwd"]
+            "oeq_rms_norm_fwd", "oeq_rms_norm_bwd", "oeq_causal_attn_workspace_size", "oeq_causal_attn_fwd",
+            "oeq_causal_attn_bwd"]
 SCHEDULES = {0: "receiver", 1: "sender"}
 
 
@@ -176,6 +177,12 @@ def lib():
     L.oeq_cross_attn_fwd.restype = st
     L.oeq_cross_attn_bwd.argtypes = [AD] + [P] * 14 + [SZ, P]
     L.oeq_cross_attn_bwd.restype = st
+    L.oeq_causal_attn_workspace_size.argtypes = [AD, SZP, SZP]
+    L.oeq_causal_attn_workspace_size.restype = st
+    L.oeq_causal_attn_fwd.argtypes = [AD] + [P] * 11 + [SZ, P]
+    L.oeq_causal_attn_fwd.restype = st
+    L.oeq_causal_attn_bwd.argtypes = [AD] + [P] * 14 + [SZ, P]
+    L.oeq_causal_attn_bwd.restype = st
     L.oeq_embedding_fwd.argtypes = [I, I64, I64, I64, P, I64, P, I32, D, P, I64, P]
     L.oeq_embedding_fwd.restype = st
     L.oeq_embedding_workspace_size.argtypes = [I, I64, I64, I64, SZP]
@@ -746,7 +753,8 @@ _LATER = {
     "readout": ("oeq_group_norm_workspace_size", "oeq_group_norm_fwd", "oeq_group_norm_bwd", "oeq_dropout_fwd",
                 "oeq_dropout_bwd", "oeq_cross_attn_workspace_size", "oeq_cross_attn_fwd", "oeq_cross_attn_bwd"),
     "decoder": ("oeq_embedding_fwd", "oeq_embedding_workspace_size", "oeq_embedding_bwd", "oeq_rms_norm_workspace_size",
-                "oeq_rms_norm_fwd", "oeq_rms_norm_e4m3_fwd", "oeq_rms_norm_bwd"),
+                "oeq_rms_norm_fwd", "oeq_rms_norm_e4m3_fwd", "oeq_rms_norm_bwd", "oeq_causal_attn_workspace_size",
+                "oeq_causal_attn_fwd", "oeq_causal_attn_bwd"),
 }
 
 

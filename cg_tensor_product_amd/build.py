@@ -23,7 +23,8 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HOST_SOURCES = ["capi.cpp", "capi_graph.cpp", "capi_edge.cpp", "capi_readout.cpp", "capi_decoder.cpp",
                 "planner.cpp", "cg_tables.cpp", "codegen.cpp", "jit.cpp"]
 HIP_SOURCES = ["csr.hip", "noalloc.hip", "group_norm.hip", "dropout.hip", "cross_attn_fwd.hip", "cross_attn_bwd.hip",
-               "embedding.hip", "rms_norm.hip"]
+               "causal_attn_fwd.hip", "causal_attn_bwd.hip",
+               "causal_attn_bwd_f32.hip", "causal_attn_bwd_f16.hip", "causal_attn_bwd_bf16.hip", "embedding.hip", "rms_norm.hip"]
 ARCH = "gfx950"
 # Accumulators of the matrix instructions in ordinary registers: the vector code between two
 # products then reads them in place.  With the default form the attention kernels moved hundreds

@@ -1,4 +1,4 @@
-// Device pieces shared by the cross-attention kernels: matrix products of 32 x 32 tiles,
+// Device pieces shared by the attention kernels (cross and causal): matrix products of 32 x 32 tiles,
 // tiles of rows in LDS and how a wave takes operands from them.
 //
 // One 32 x 32 x 16 step multiplies A [32, 16] by B [16, 32].  Lane l holds, with
@@ -204,17 +204,32 @@ struct Place {
     bool any;
 };
 
-template <int kTile>
+// kCausal: the longest walks come first, those of the last query rows and of the first keys (an even
+// end: 4 x 1024 rows FIGORDER), and the key heads of a tile follow each other, so that with eight heads, or
+// four, an XCD's workgroups read one head's keys.
+template <int kTile, bool kCausal = false>
 __device__ __forceinline__ Place place_of(const AttnArgs &a, uint32_t item, bool by_query, int splits, int64_t n_slots) {
     Place p;
     const uint32_t slots = static_cast<uint32_t>(n_slots), rest = item / static_cast<uint32_t>(splits);
     p.split = static_cast<int>(item - rest * splits);
-    p.kv_head = static_cast<int>(rest / slots);
-    const int64_t slot = rest - p.kv_head * slots;
+    int64_t slot;
+    if (kCausal) {
+        const uint32_t kv_heads = static_cast<uint32_t>(a.kv_heads), tile = rest / kv_heads;
+        p.kv_head = static_cast<int>(rest - tile * kv_heads);
+        slot = by_query ? slots - 1 - tile : tile;
+    } else {
+        p.kv_head = static_cast<int>(rest / slots);
+        slot = rest - p.kv_head * slots;
+    }
     const Owner at_slot = by_query ? find_structure(a.q_ptr, a.k_ptr, a.n_struct, a.share, kTile, slot)
                                    : find_structure(a.k_ptr, a.q_ptr, a.n_struct, 1, kTile, slot);
     const int32_t *qp = by_query ? at_slot.ptr : at_slot.other, *kp = by_query ? at_slot.other : at_slot.ptr;
-    const Span q = span_of(qp[0], qp[1], a.q_rows), k = span_of(kp[0], kp[1], a.k_rows);
+    const Span q = span_of(qp[0], qp[1], a.q_rows);
+    Span k = span_of(kp[0], kp[1], a.k_rows);
+    if (kCausal && a.k_len) {
+        const int64_t n = a.k_len[at_slot.index];
+        k.end = min(k.end, k.begin + max(n, int64_t(0)));
+    }
     p.q_begin = q.begin;
     p.k_begin = k.begin;
     p.rows = static_cast<int>((q.end - q.begin) * a.share);
@@ -223,6 +238,61 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a, uint32_t item, bool
     p.first = static_cast<int>(at);
     p.any = at >= 0 && at < (by_query ? p.rows : p.keys);
     return p;
+}
+
+// Causal visibility: query i of n sees the keys j <= i + `off`, off = keys - n.  Row r of a workgroup's key head
+// is query r / share.
+__device__ __forceinline__ int causal_offset(const AttnArgs &a, const Place &w) { return w.keys - w.rows / a.share; }
+
+// The lowest n bits (n < 0: none).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0 : (1ull << n) - 1; }
+
+// A walk with care, where the causal limit cuts a tile: the products take the tile's infinities and NaNs as zeros
+// (`finite_only`), and `add_others` adds them, row by row of the tile, to the sums of the lanes whose bit of `used`
+// is set; kNan: as NaN, for a factor of either sign.
+template <class T>
+__device__ __forceinline__ vec8<T> finite_only(vec8<T> v) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.f;
+        return v;
+    } else {
+        constexpr short kExponent = std::is_same<T, f16>::value ? 0x7C00 : 0x7F80;
+        i16x8 w = __builtin_bit_cast(i16x8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = (w[i] & kExponent) == kExponent ? short(0) : w[i];
+        return __builtin_bit_cast(vec8<T>, w);
+    }
+}
+template <bool kNan, class T, int kOut>
+__device__ __forceinline__ void add_others(f32x16 (&sum)[kOut], const T *tile, int tile_row, uint32_t used, int half) {
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+        const bool sees = used >> j & 1;
+        const T *row = tile + j * tile_row + 4 * half;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = static_cast<float>(row[32 * d + 8 * (i >> 2) + (i & 3)]);
+                if (sees && !(fabsf(x) < INFINITY)) sum[d][i] += kNan ? x - x : x;
+            }
+        }
+    }
+}
+
+// Whether all sums are finite (they are far from where their own sum would not be).
+template <int kOut>
+__device__ __forceinline__ bool finite(const f32x16 (&sum)[kOut]) {
+    f32x16 all = sum[0];
+#pragma unroll
+    for (int d = 1; d < kOut; ++d) all += sum[d];
+#pragma unroll
+    for (int n = 8; n > 0; n >>= 1) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) all[i] += all[n + i];
+    }
+    return fabsf(all[0]) < INFINITY;
 }
 
 }  // namespace readout

@@ -51,6 +51,14 @@ oeq_status check_rows(const void *p, int64_t stride, int32_t n_cols, size_t size
     return check_aligned(p, size, name);
 }
 
+oeq_status causal_args(const oeq_attn_desc *desc, ro::AttnArgs *a) {
+    OEQ_TRY(attn_args(desc, a, ro::causal_attn_fwd_blocks, ro::causal_attn_bwd_blocks));
+    // the walks count rows up to a tile of keys past a sequence's last query
+    if (desc->q_rows + 256 >= (int64_t(1) << 31) / desc->n_heads)
+        return fail(OEQ_ERR_UNSUPPORTED, "query rows times heads must stay 256 rows below 2^31");
+    return OEQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,6 +172,57 @@ oeq_status oeq_rms_norm_bwd(oeq_dtype dtype, int64_t n_rows, int32_t n_cols, con
         a.grad_sum = grad_sum, a.ld_grad_sum = grad_sum_stride, a.grad_x = grad_x, a.ld_grad_x = grad_x_stride;
         a.grad_weight = grad_weight, a.workspace = workspace;
         return from_hip(ro::rms_norm_bwd(dtype, a, static_cast<hipStream_t>(stream)), "rms norm backward");
+    });
+}
+
+oeq_status oeq_causal_attn_workspace_size(const oeq_attn_desc *desc, size_t *fwd_bytes, size_t *bwd_bytes) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(causal_args(desc, &a));
+        if (fwd_bytes) *fwd_bytes = a.n_struct && a.q_rows ? ro::causal_attn_fwd_workspace(desc->dtype, a) : 0;
+        if (bwd_bytes) *bwd_bytes = a.n_struct ? ro::causal_attn_bwd_workspace(desc->dtype, a) : 0;
+        return OEQ_OK;
+    });
+}
+
+oeq_status oeq_causal_attn_fwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr,
+                               const int32_t *k_len, const void *q, const void *k, const void *v,
+                               const uint8_t *key_mask, const int64_t *rng, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(causal_args(desc, &a));
+        OEQ_TRY(attn_operands(&a, q_ptr, k_ptr, q, k, v, key_mask, rng));
+        OEQ_TRY(check_aligned(k_len, 4, "k_len"));
+        if (a.q_rows == 0) return OEQ_OK;
+        if (!out || !lse) return fail(OEQ_ERR_INVALID_ARG, "out or lse is NULL");
+        OEQ_TRY(check_aligned(out, 16, "out"));
+        OEQ_TRY(check_aligned(lse, 4, "lse"));
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::causal_attn_fwd_workspace(desc->dtype, a)));
+        a.k_len = k_len, a.out = out, a.lse = lse, a.workspace = workspace;
+        return from_hip(ro::causal_attn_fwd(desc->dtype, a, static_cast<hipStream_t>(stream)), "causal attention");
+    });
+}
+
+oeq_status oeq_causal_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, const int32_t *k_ptr, const void *q,
+                               const void *k, const void *v, const uint8_t *key_mask, const int64_t *rng,
+                               const void *out, const float *lse, const void *grad_out, void *grad_q, void *grad_k,
+                               void *grad_v, void *workspace, size_t workspace_bytes, void *stream) {
+    return guarded([&]() -> oeq_status {
+        ro::AttnArgs a;
+        OEQ_TRY(causal_args(desc, &a));
+        OEQ_TRY(attn_operands(&a, q_ptr, k_ptr, q, k, v, key_mask, rng));
+        if (a.q_rows && (!out || !lse || !grad_out)) return fail(OEQ_ERR_INVALID_ARG, "out, lse or grad_out is NULL");
+        for (const void *p : {out, grad_out, static_cast<const void *>(grad_q), static_cast<const void *>(grad_k),
+                              static_cast<const void *>(grad_v)})
+            OEQ_TRY(check_aligned(p, 16, "out, grad_out and the gradients"));
+        OEQ_TRY(check_aligned(lse, 4, "lse"));
+        if (a.n_struct == 0 || (!grad_q && !grad_k && !grad_v)) return OEQ_OK;
+        OEQ_TRY(check_workspace(workspace, workspace_bytes, ro::causal_attn_bwd_workspace(desc->dtype, a)));
+        a.out = const_cast<void *>(out), a.lse = const_cast<float *>(lse), a.grad_out = grad_out;
+        a.grad_q = grad_q, a.grad_k = grad_k, a.grad_v = grad_v, a.workspace = workspace;
+        return from_hip(ro::causal_attn_bwd(desc->dtype, a, static_cast<hipStream_t>(stream)),
+                        "causal attention backward");
     });
 }
 

@@ -104,6 +104,7 @@ struct AttnArgs {
     int32_t dim;
     int64_t q_rows, k_rows;
     const int32_t *q_ptr, *k_ptr;
+    const int32_t *k_len;     // causal forward: states in use of each structure; may be NULL (all)
     const uint8_t *key_mask;  // may be NULL
     const void *q, *k, *v;
     int64_t q_row, q_head, k_row, k_head, v_row, v_head;  // strides
@@ -124,6 +125,13 @@ int64_t cross_attn_fwd_blocks(oeq_dtype dtype, const AttnArgs &a);
 int64_t cross_attn_bwd_blocks(oeq_dtype dtype, const AttnArgs &a);
 hipError_t cross_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
 hipError_t cross_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
+// The same with the causal limit.
+size_t causal_attn_fwd_workspace(oeq_dtype dtype, const AttnArgs &a);
+size_t causal_attn_bwd_workspace(oeq_dtype dtype, const AttnArgs &a);
+int64_t causal_attn_fwd_blocks(oeq_dtype dtype, const AttnArgs &a);
+int64_t causal_attn_bwd_blocks(oeq_dtype dtype, const AttnArgs &a);
+hipError_t causal_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
+hipError_t causal_attn_bwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream);
 
 }  // namespace readout
 }  // namespace oeq

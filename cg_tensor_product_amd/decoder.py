@@ -10,7 +10,8 @@ import functools
 import torch
 
 from . import _check, lib
-from .readout import (_DTYPES, _F32, _I64, _dense, _head, _like, _number, _raw_stream, _row_stride, _scratch, _typed)
+from .readout import (_DTYPES, _F32, _I32, _I64, _attn, _attn_desc, _dense, _head, _like, _raw_stream, _row_stride, _scratch,
+                      _typed)
 
 _E4M3 = torch.float8_e4m3fn
 
@@ -181,3 +182,56 @@ def oeq_rms_norm_bwd(sum, rstd, grad_out, weight=None, grad_sum=None, need=("x",
     if st:
         _check(st)
     return gx, gw
+
+
+# ---------------------------------------------------------------------------
+# causal attention
+# ---------------------------------------------------------------------------
+
+def oeq_causal_attn_workspace_size(q_shape, k_shape, n_struct: int, dtype=torch.float32):
+    """Workspace bytes (forward, backward) for q of shape [Tq, H, D] and k, v of [Tk, Hkv, D]."""
+    (tq, h, d), (tk, hk, _) = q_shape, k_shape
+    return _attn_desc(True, _DTYPES[dtype], n_struct, h, hk, d, tq, tk, 0, 0, 0, 0, 0, 0, 1.0, 0.0)[1:]
+
+
+def oeq_causal_attn_fwd(q, k, v, q_ptr, k_ptr, scale=None, key_mask=None, k_len=None, p_drop: float = 0.0, rng=None,
+                        out=None, lse=None, workspace=None):
+    """(out, lse): causal attention of q [Tq, H, D] to the states k, v [Tk, Hkv, D] of their sequence
+    (q_ptr, k_ptr: int32 row pointers over the same sequences; the last query stands at the last
+    state).  k_len (int32 [sequences]): the states in use of each, the first of its rows, for caches
+    with rows to spare.  The other arguments are those of oeq_cross_attn_fwd."""
+    dev, (desc, fwd_bytes, _), operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng, True)
+    used = _dense(k_len, (q_ptr.shape[0] - 1,), _I32, dev, "k_len")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _dense(out, q.shape, q.dtype, dev, "out")
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    else:
+        _dense(lse, q.shape[:2], _F32, dev, "lse")
+    keep, ws, nbytes = _scratch(fwd_bytes, workspace, q.device)
+    st = lib().oeq_causal_attn_fwd(desc, *operands[:2], used, *operands[2:], out.data_ptr(), lse.data_ptr(), ws, nbytes,
+                                   _raw_stream(dev))
+    if st:
+        _check(st)
+    return out, lse
+
+
+def oeq_causal_attn_bwd(q, k, v, q_ptr, k_ptr, out, lse, grad_out, scale=None, key_mask=None, p_drop: float = 0.0,
+                        rng=None, need=("q", "k", "v"), grads=None, workspace=None):
+    """(grad_q, grad_k, grad_v) of <grad_out, out> from the forward's operands (without k_len), out and lse;
+    entries not in `need` are None.  `grads` may supply preallocated gradients (contiguous)."""
+    dev, (desc, _, bwd_bytes), operands = _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng, True)
+    saved = (_dense(out, q.shape, q.dtype, dev, "out"), _dense(lse, q.shape[:2], _F32, dev, "lse"),
+             _dense(grad_out, q.shape, q.dtype, dev, "grad_out"))
+    if grads is None:
+        grads = tuple(torch.empty_like(t, memory_format=torch.contiguous_format) if n in need else None
+                      for n, t in (("q", q), ("k", k), ("v", k)))
+    addresses = tuple(_dense(g, t.shape, q.dtype, dev, n)
+                      for g, t, n in zip(grads, (q, k, k), ("grad_q", "grad_k", "grad_v")))
+    keep, ws, nbytes = _scratch(bwd_bytes, workspace, q.device)
+    st = lib().oeq_causal_attn_bwd(desc, *operands, *saved, *addresses, ws, nbytes, _raw_stream(dev))
+    if st:
+        _check(st)
+    return tuple(grads)

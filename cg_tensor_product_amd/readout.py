@@ -256,21 +256,22 @@ def _number(v, name):
 
 
 @functools.lru_cache(maxsize=4096)
-def _attn_desc(*fields):
+def _attn_desc(causal, *fields):
     """(descriptor, workspace bytes forward, backward), a function of sizes, strides and numbers."""
     d = _AttnDesc(*fields)
     f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().oeq_cross_attn_workspace_size(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b)))
+    size = lib().oeq_causal_attn_workspace_size if causal else lib().oeq_cross_attn_workspace_size
+    _check(size(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b)))
     return ctypes.byref(d), f.value, b.value
 
 
 def oeq_cross_attn_workspace_size(q_shape, k_shape, n_struct: int, dtype=torch.float32):
     """Workspace bytes (forward, backward) for q of shape [Tq, H, D] and k, v of [Tk, Hkv, D]."""
     (tq, h, d), (tk, hk, _) = q_shape, k_shape
-    return _attn_desc(_DTYPES[dtype], n_struct, h, hk, d, tq, tk, 0, 0, 0, 0, 0, 0, 1.0, 0.0)[1:]
+    return _attn_desc(False, _DTYPES[dtype], n_struct, h, hk, d, tq, tk, 0, 0, 0, 0, 0, 0, 1.0, 0.0)[1:]
 
 
-def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
+def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng, causal=False):
     """(device, what _attn_desc gives, addresses of the operands both directions read)"""
     code, dev = _head(q, "q")
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -285,7 +286,7 @@ def _attn(q, k, v, q_ptr, k_ptr, scale, key_mask, p_drop, rng):
     mask = None
     if key_mask is not None:
         mask = _dense(key_mask, (tk,), torch.bool if key_mask.dtype is torch.bool else _U8, dev, "key_mask")
-    desc = _attn_desc(code, B, h, hk, d, tq, tk, *_heads(q, shape, dt, dev, "q"), *_heads(k, kv, dt, dev, "k"),
+    desc = _attn_desc(causal, code, B, h, hk, d, tq, tk, *_heads(q, shape, dt, dev, "q"), *_heads(k, kv, dt, dev, "k"),
                       *_heads(v, kv, dt, dev, "v"), d ** -0.5 if scale is None else _number(scale, "scale"),
                       _number(p_drop, "p_drop"))
     return dev, desc, (q_ptr.data_ptr(), k_ptr.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), mask,

@@ -637,6 +637,34 @@ oeq_status oeq_rms_norm_bwd(oeq_dtype dtype, int64_t n_rows, int32_t n_cols, con
                             float *grad_weight, void *workspace, size_t workspace_bytes,
                             void *stream);
 
+/* Causal attention over packed sequences, with the cross attention's descriptor, layouts and
+ * rounding: sequence b has the query rows q_ptr[b]..q_ptr[b+1] and the states
+ * k_ptr[b]..k_ptr[b+1], and its last query stands at its last state.  Query i of n in a sequence
+ * of m states sees the states j <= i + m - n that key_mask leaves: a whole prompt (q_ptr and
+ * k_ptr alike), a chunk of one over the states before it, or one token over its cache (n = 1).
+ * Queries before the first state (n > m) see nothing: out = 0, lse = -infinity.  States that a
+ * query does not see have no part in its results, whatever they hold.
+ *   k_len (int32 [n_struct], NULL: all): the states in use of each sequence, the first ones of its
+ *   rows, for caches with rows to spare; m = max(0, min(k_len[b], k_ptr[b+1] - k_ptr[b])).  The
+ *   backward takes no spare rows.
+ * The dropout's column is the state's number within the sequence, as in the cross attention. */
+oeq_status oeq_causal_attn_workspace_size(const oeq_attn_desc *desc, size_t *fwd_bytes,
+                                          size_t *bwd_bytes);
+oeq_status oeq_causal_attn_fwd(const oeq_attn_desc *desc, const int32_t *q_ptr,
+                               const int32_t *k_ptr, const int32_t *k_len, const void *q,
+                               const void *k, const void *v, const uint8_t *key_mask,
+                               const int64_t *rng, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Gradients of <grad_out, out>, as in oeq_cross_attn_bwd; what the forward did not see has no
+ * part in them, and states that no query sees get zeros. */
+oeq_status oeq_causal_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr,
+                               const int32_t *k_ptr, const void *q, const void *k, const void *v,
+                               const uint8_t *key_mask, const int64_t *rng, const void *out,
+                               const float *lse, const void *grad_out, void *grad_q, void *grad_k,
+                               void *grad_v, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
 /* Synchronously validates a receiver CSR on the device (rowptr monotone,
  * rowptr[0] = 0, rowptr[N] = E, 0 <= src < N).  Test helper: synchronises. */
 oeq_status oeq_csr_check(int64_t n_nodes, int64_t n_edges, const int32_t *rowptr,

@@ -110,3 +110,64 @@ def test_rms_norm_workspace_sizes():
     assert size(0, 64, ctypes.byref(b)) == 0 and b.value == 0
     assert size(10, 4096, ctypes.byref(b)) == 0 and b.value >= 4096 * 4
     assert size(10, 0, ctypes.byref(b)) == 1 and size(-1, 8, None) == 1 and size(10, 16385, None) == 2
+
+
+# ---- causal attention -------------------------------------------------------------------------
+
+FIELDS = dict(dtype=0, n_struct=2, n_heads=4, n_kv_heads=2, head_dim=16, q_rows=6, k_rows=9, q_stride=64,
+              q_head_stride=16, k_stride=32, k_head_stride=16, v_stride=32, v_head_stride=16, scale=0.25, p_drop=0.0)
+
+
+def _desc(**kw):
+    return oeq._AttnDesc(*{**FIELDS, **kw}.values())
+
+
+def _attn(desc, q_ptr=A, k_ptr=A, k_len=None, q=A, k=A, v=A, mask=None, rng=None, out=A, lse=A, ws=None, wsb=0):
+    return oeq.lib().oeq_causal_attn_fwd(None if desc is None else ctypes.byref(desc), q_ptr, k_ptr, k_len, q, k, v, mask,
+                                         rng, out, lse, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=1), 2), (dict(n_struct=-1), 1), (dict(n_struct=0), 1), (dict(n_heads=3), 1), (dict(n_heads=0), 1),
+    (dict(n_kv_heads=0), 1), (dict(head_dim=0), 1), (dict(head_dim=12), 2), (dict(head_dim=136), 2),
+    (dict(q_rows=-1), 1), (dict(k_rows=-1), 1), (dict(q_rows=2**29), 2), (dict(q_rows=2**29 - 256), 2),
+    (dict(k_rows=2**31), 2), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(p_drop=1.0), 1),
+    (dict(p_drop=0.1), 1), (dict(q_stride=66), 1), (dict(k_stride=-32), 1), (dict(v_head_stride=2), 1),
+    (dict(n_struct=1 << 26, n_heads=64, n_kv_heads=64), 2),
+])
+def test_causal_attn_descriptor_refusals(kw, status):
+    assert _attn(_desc(**kw)) == status, _message()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q_ptr=None), 1), (dict(k_ptr=None), 1), (dict(k_len=P(4098)), 1), (dict(q=None), 1), (dict(k=None), 1),
+    (dict(v=None), 1), (dict(out=None), 1), (dict(lse=None), 1), (dict(q=P(4104)), 1), (dict(k=P(4100)), 1),
+    (dict(out=P(4100)), 1), (dict(q_ptr=P(4098)), 1),
+])
+def test_causal_attn_operand_refusals(kw, status):
+    assert _attn(_desc(), **kw) == status, _message()
+    assert _attn(None) == 1
+
+
+def test_causal_attn_backward_refusals():
+    def call(desc=_desc(), out=A, lse=A, go=A, gq=A, gk=A, gv=A, ws=None, wsb=0):
+        return oeq.lib().oeq_causal_attn_bwd(ctypes.byref(desc), A, A, A, A, A, None, None, out, lse, go, gq, gk, gv, ws,
+                                             wsb, None)
+
+    assert call(out=None) == 1 and call(lse=None) == 1 and call(go=None) == 1
+    assert call(gk=P(4104)) == 1 and call(go=P(4104)) == 1
+    assert call(gq=None, gk=None, gv=None) == 0  # nothing asked for
+    assert call() == 3 and call(ws=P(4104), wsb=1 << 40) == 3  # delta needs a workspace
+
+
+def test_causal_attn_workspace_sizes():
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    size = oeq.lib().oeq_causal_attn_workspace_size
+    assert size(ctypes.byref(_desc()), ctypes.byref(f), ctypes.byref(b)) == 0 and f.value == 0
+    assert b.value >= 6 * 4 * 4  # delta
+    d = _desc(n_struct=1, q_rows=1, k_rows=100000)  # long states, few rows: outputs and log sums of each split
+    assert size(ctypes.byref(d), ctypes.byref(f), None) == 0 and f.value >= 2 * 4 * (16 + 1) * 4
+    assert _attn(d) == 3
+    empty = _desc(n_struct=0, q_rows=0, k_rows=0)
+    assert size(ctypes.byref(empty), ctypes.byref(f), ctypes.byref(b)) == 0 and f.value == b.value == 0
+    assert _attn(empty, q_ptr=None, k_ptr=None, q=None, k=None, v=None, out=None, lse=None) == 0
