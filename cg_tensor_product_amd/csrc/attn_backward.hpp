@@ -121,7 +121,17 @@ struct Bwd {
     int64_t q_slots, k_slots;
     int64_t key_blocks;  // workgroups that own keys; the rest own query rows
     float *delta;        // causal: [query row, head], as the accumulators start from it
+    // causal: walks are cut into pieces of about this many tiles, at most q_splits (k_splits) of them; [query row,
+    // head] and [key, key head]: into how many
+    int piece;
+    int32_t *q_pieces, *k_pieces;
 };
+
+// The waves' keys or rows of a workgroup, as in the forward.
+template <bool kCausal>
+__device__ __forceinline__ int part_of(int wave) {
+    return kCausal && (blockIdx.x >> 8 & 1) ? kWaves - 1 - wave : wave;
+}
 
 // p from a score, times 2^bits where `lse` is less by that; fp32 forms scale s - lse in one
 // rounding, since the difference is small against its parts.  `lse` is in powers of two for 16-bit
@@ -210,8 +220,8 @@ __device__ __forceinline__ float sum_half(float v) {
 template <class T, int kDim, bool kDrop, bool kExact, bool kCare, bool kCausal>
 __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, const Place &w, int tid, KeyLds<T, kDim> &lds) {
     constexpr int kRow = KeyLds<T, kDim>::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const int lane = tid & 63, half = lane >> 5, wave = tid >> 6;
-    const int key = w.first + wave * 32 + (lane & 31);
+    const int lane = tid & 63, half = lane >> 5, wave = tid >> 6, key_base = w.first + part_of<kCausal>(wave) * 32;
+    const int key = key_base + (lane & 31);
     const bool key_ok = key < w.keys;
     const int64_t k_row = w.k_begin + (key_ok ? key : 0);
     const bool seen = key_ok && (!a.key_mask || a.key_mask[k_row]);
@@ -225,13 +235,19 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
     // and those of the wave's first and last keys
     int t_first = 0, see_from = 0, wave_first = 0, wave_last = 0;
     if (kCausal) {
-        const int off = causal_offset(a, w), base = w.first + wave * 32;
+        const int off = causal_offset(a, w);
         t_first = min(n_tiles, max(0, w.first - off) * a.share / kRowTile);
         see_from = max(0, key - off) * a.share;
-        wave_first = __builtin_amdgcn_readfirstlane(max(0, base - off) * a.share);
-        wave_last = __builtin_amdgcn_readfirstlane(max(0, base + 31 - off) * a.share);
+        wave_first = __builtin_amdgcn_readfirstlane(max(0, key_base - off) * a.share);
+        wave_last = __builtin_amdgcn_readfirstlane(max(0, key_base + 31 - off) * a.share);
     }
-    const int per = (n_tiles - t_first + out.k_splits - 1) / out.k_splits;
+    int pieces = out.k_splits;
+    if (kCausal && pieces > 1) {
+        pieces = max(1, min(pieces, (n_tiles - t_first + out.piece - 1) / out.piece));
+        if (w.split >= pieces) return true;
+        if (w.split == 0 && half == 0 && key_ok) out.k_pieces[k_row * a.kv_heads + w.kv_head] = pieces;
+    }
+    const int per = (n_tiles - t_first + pieces - 1) / pieces;
     const int t_end = min(n_tiles, t_first + (w.split + 1) * per);
     const auto row_of = [&](int r, int64_t *q_row) {  // rows past the end: the last one
         r = min(r, w.rows - 1);
@@ -342,7 +358,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
             int64_t q_row;
             const int head = row_of(r0 + (lane & 31), &q_row);
             const uint32_t row = static_cast<uint32_t>(q_row * a.heads + head);
-            const uint32_t block = static_cast<uint32_t>(w.first + wave * 32) / 8 + 2 * half;
+            const uint32_t block = static_cast<uint32_t>(key_base) / 8 + 2 * half;
             const uint32_t bits = keep_bits(g, block, row, a.threshold) | keep_bits(g, block + 1, row, a.threshold) << 8;
             reinterpret_cast<uint16_t *>(lds.kept[wave])[(lane & 31) * 2 + half] = static_cast<uint16_t>(bits);
         }
@@ -456,7 +472,7 @@ __device__ __forceinline__ bool grad_keys(const AttnArgs &a, const Bwd &out, con
         if (max_wave<1>(__any(seen && !(finite(gk) && (!kCausal || finite(gv)))))) return false;
     }
     if (!key_ok) return true;
-    const bool split = out.k_splits > 1;
+    const bool split = pieces > 1;
     const int64_t at = (split ? int64_t(w.split) * a.k_rows * a.kv_heads : 0) + k_row * a.kv_heads + w.kv_head;
     const float k_factor = a.scale * a.keep_scale * power(-bits - kProb);
     const float v_factor = a.keep_scale * power(kScaled<T> && !kCare ? -bits - kProb : -kProb);
@@ -494,27 +510,39 @@ struct QueryTiles {
 
 // The waves share tiles of keys, or with kSplitKeys (few query rows) take them in turn, as in
 // the forward.  kExact: the structure has kExactStates keys at most, one tile, and delta is its sum of p dp.
-template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kExact, bool kCausal>
-__device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, const Place &w, char *lds) {
+// Causal without kCare: false, without results, where the walk is to be done again with care.  `tid` is threadIdx.x.
+template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kExact, bool kCausal, bool kCare>
+__device__ __forceinline__ bool grad_queries(const AttnArgs &a, const Bwd &out, const Place &w, int tid, char *lds) {
     using C = QueryTiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32;
-    const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
-    const int thread = kSplitKeys ? lane : threadIdx.x;
+    const int lane = tid & 63, half = lane >> 5, wave = tid >> 6;
+    const int thread = kSplitKeys ? lane : tid;
     T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
 
     static_assert(kKeys >= kExactStates, "one tile");
-    const int r = w.first + (kSplitKeys ? 0 : wave * 32) + (lane & 31);
+    const int base = w.first + (kSplitKeys ? 0 : part_of<kCausal>(wave) * 32), r = base + (lane & 31);
     const bool row_ok = r < w.rows;
     // causal: as in the forward
     int keys = w.keys, limit = 0, wave_first = 0, wave_last = 0;
     if (kCausal) {
-        const int off = causal_offset(a, w), most = w.rows - 1, base = w.first + (kSplitKeys ? 0 : wave * 32);
+        const int off = causal_offset(a, w), most = w.rows - 1;
         keys = max(0, min(keys, min(w.first + C::kRows - 1, most) / a.share + off + 1));
         limit = min(r, most) / a.share + off;
         wave_first = __builtin_amdgcn_readfirstlane(min(base, most) / a.share + off);
         wave_last = __builtin_amdgcn_readfirstlane(min(base + 31, most) / a.share + off);
     }
-    const int splits = out.q_splits, n_tiles = (keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
+    const int n_tiles = (keys + kKeys - 1) / kKeys;
+    int splits = out.q_splits;
+    if (kCausal && splits > 1) {
+        splits = max(1, min(splits, (n_tiles + out.piece - 1) / out.piece));
+        if (w.split >= splits) return true;
+        if (w.split == 0 && tid < C::kRows) {
+            const int row = w.first + static_cast<int>(tid);
+            if (row < w.rows)
+                out.q_pieces[(w.q_begin + row / a.share) * a.heads + w.kv_head * a.share + row % a.share] = splits;
+        }
+    }
+    const int per = (n_tiles + splits - 1) / splits;
     const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
     const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
@@ -558,7 +586,6 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 
     // kMost: for the largest score gradient of each row alone, without the power
     float most = 0.f;
-    bool care = false;  // causal: a walk again
     const auto walk = [&](auto kind) {
         constexpr bool kMost = decltype(kind)::value;
         const float p_lse = lse - (kScaled<T> && !kMost ? float(bits) : 0.f);
@@ -635,7 +662,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
                 if (!kMost) two_terms<T>(s8, &sf[h], &sl[h]);
             }
             if constexpr (!kMost) {
-                const bool careful = kCausal && care && cut;
+                const bool careful = kCare && cut;
 #pragma unroll
                 for (int d = 0; d < kOut; ++d) {
 #pragma unroll
@@ -661,18 +688,25 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
 #pragma unroll
         for (int d = 0; d < kOut; ++d) gq[d] = f32x16{};
         walk(std::false_type());
-        if constexpr ((!kScaled<T> || kExact) && !kCausal) break;
+        if constexpr (kCausal) {
+            if constexpr (!kCare) {
+                if (max_wave<3>(__any(row_ok && !finite(gq)))) return false;
+                break;
+            } else if constexpr (!kScaled<T>) {
+                break;
+            } else {
+                if (again) break;
+            }
+        }
+        if constexpr (!kScaled<T> || kExact) break;
         const bool lost = max_halves(finite(gq) ? 0.f : 1.f) > 0.f;  // the row, whose columns are in both halves
         const int any = __any(lost);
         if (again || !(kSplitKeys ? any : max_wave<2>(any))) break;
-        care = true;
-        if constexpr (kScaled<T>) {
-            in.fetch(a, k_base, v_base, mask, keys, t_begin);
-            walk(std::true_type());
-            most = max_halves(most);
-            if (lost) bits = bits_for(most);
-            if (!kSplitKeys) __syncthreads();  // before the first buffer is written again
-        }
+        in.fetch(a, k_base, v_base, mask, keys, t_begin);
+        walk(std::true_type());
+        most = max_halves(most);
+        if (lost) bits = bits_for(most);
+        if (!kSplitKeys) __syncthreads();  // before the first buffer is written again
         in.fetch(a, k_base, v_base, mask, keys, t_begin);
     }
     if (kScaled<T>) {
@@ -683,7 +717,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
     const int64_t part = split ? int64_t(w.split) * a.q_rows * a.heads : 0;
     const float factor = a.scale * a.keep_scale;
     if (!kSplitKeys) {
-        if (!row_ok) return;
+        if (!row_ok) return true;
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
@@ -693,7 +727,7 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
                 if (col < a.dim) put4<T>(split ? out.part_q : nullptr, a.grad_q, (part + at) * a.dim + col, v * factor);
             }
         }
-        return;
+        return true;
     }
     __syncthreads();
     float *join = reinterpret_cast<float *>(lds), *mine = join + (wave * 32 + (lane & 31)) * C::kJoinRow;
@@ -706,10 +740,10 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
         }
     }
     __syncthreads();
-    const int jr = threadIdx.x >> 3, jrow = w.first + jr;  // eight threads a row
-    if (jrow >= w.rows) return;
+    const int jr = tid >> 3, jrow = w.first + jr;  // eight threads a row
+    if (jrow >= w.rows) return true;
     const int64_t to = (w.q_begin + jrow / a.share) * a.heads + w.kv_head * a.share + jrow % a.share;
-    for (int col = (threadIdx.x & 7) * 8; col < a.dim; col += 64) {
+    for (int col = (tid & 7) * 8; col < a.dim; col += 64) {
         f32x8 v = {};
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
@@ -723,6 +757,26 @@ __device__ __forceinline__ void grad_queries(const AttnArgs &a, const Bwd &out, 
         else
             store8(static_cast<T *>(a.grad_q) + to * a.dim + col, from_f32<T>(v));
     }
+    return true;
+}
+
+struct BackwardArgs {
+    AttnArgs a;
+    Bwd out;
+};
+
+template <class T, int kDim, bool kDrop>
+__device__ __attribute__((noinline)) void keys_with_care(const Passed<BackwardArgs> *passed, char *lds) {
+    const BackwardArgs b = passed->get();
+    const Place w = place_of<kKeyTile, true>(b.a, blockIdx.x, false, b.out.k_splits, b.out.k_slots, false);
+    grad_keys<T, kDim, kDrop, false, true, true>(b.a, b.out, w, threadIdx.x, *reinterpret_cast<KeyLds<T, kDim> *>(lds));
+}
+template <class T, int kDim, bool kDrop, bool kSplitKeys>
+__device__ __attribute__((noinline)) void queries_with_care(const Passed<BackwardArgs> *passed, char *lds) {
+    const BackwardArgs b = passed->get();
+    const uint32_t item = blockIdx.x - static_cast<uint32_t>(b.out.key_blocks);
+    const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows, true>(b.a, item, true, b.out.q_splits, b.out.q_slots, false);
+    grad_queries<T, kDim, kDrop, kSplitKeys, false, true, true>(b.a, b.out, w, threadIdx.x, lds);
 }
 
 // Three workgroups a compute unit for fp16 at D = 32 (with dropout, 64 structures of up to 32 rows and 200
@@ -735,32 +789,63 @@ __global__ void __launch_bounds__(kThreads, (kScaled<T> && kDim <= 32) ? 3 : (si
     constexpr int kKeyBytes = int(sizeof(KeyLds<T, kDim>)), kQueryBytes = QueryTiles<T, kDim, kSplitKeys>::kBytes;
     __shared__ __attribute__((aligned(16))) char lds[kKeyBytes > kQueryBytes ? kKeyBytes : kQueryBytes];
     uint32_t block = blockIdx.x;
+    if constexpr (kCausal) {
+        bool done = true;
+        const bool keys = block < out.key_blocks;
+        if (keys) {
+            const Place w = place_of<kKeyTile, true>(a, block, false, out.k_splits, out.k_slots, false);
+            if (!w.any) return;
+            // (of fp16 a walk of one tile is done with care at once, as in the cross attention)
+            done = kScaled<T> && w.rows <= kRowTile
+                       ? false
+                       : grad_keys<T, kDim, kDrop, false, false, true>(a, out, w, threadIdx.x,
+                                                                       *reinterpret_cast<KeyLds<T, kDim> *>(lds));
+        } else {
+            const uint32_t item = block - static_cast<uint32_t>(out.key_blocks);
+            const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows, true>(a, item, true, out.q_splits, out.q_slots, false);
+            if (!w.any) return;
+            done = grad_queries<T, kDim, kDrop, kSplitKeys, false, true, false>(a, out, w, threadIdx.x, lds);
+        }
+        if (!done) {
+            __shared__ Passed<BackwardArgs> passed;
+            if (threadIdx.x == 0) passed.put({a, out});
+            __syncthreads();
+            if (keys)
+                keys_with_care<T, kDim, kDrop>(&passed, lds);
+            else
+                queries_with_care<T, kDim, kDrop, kSplitKeys>(&passed, lds);
+        }
+        return;
+    }
     if (block < out.key_blocks) {
         KeyLds<T, kDim> &tiles = *reinterpret_cast<KeyLds<T, kDim> *>(lds);
         int tid = threadIdx.x;
-        const auto place = [&]() { return place_of<kKeyTile, kCausal>(a, block, false, out.k_splits, out.k_slots); };
+        const auto place = [&]() { return place_of<kKeyTile>(a, block, false, out.k_splits, out.k_slots); };
         const Place w = place();
         if (!w.any) return;
         if (kExactDelta<T, kCausal> && w.keys <= kExactStates) {
-            grad_keys<T, kDim, kDrop, kExactDelta<T, kCausal>, kScaled<T>, kCausal>(a, out, w, tid, tiles);
+            grad_keys<T, kDim, kDrop, kExactDelta<T, kCausal>, kScaled<T>, false>(a, out, w, tid, tiles);
         } else if ((kScaled<T> && w.rows <= kRowTile) ||
-                   !grad_keys<T, kDim, kDrop, false, false, kCausal>(a, out, w, tid, tiles)) {
+                   !grad_keys<T, kDim, kDrop, false, false, false>(a, out, w, tid, tiles)) {
             // (a walk of one tile is done with care at once: fp16, 64 structures of up to 32 rows and 200
             // states, D = 32 with dropout 21.2 -> 19.9 us)
-            if constexpr (kScaled<T> || kCausal) {
+            if constexpr (kScaled<T>) {
                 // finds its place and its thread anew: kept for this, they would take registers of the other walk
                 asm volatile("" : "+s"(block), "+v"(tid));
-                grad_keys<T, kDim, kDrop, false, true, kCausal>(a, out, place(), tid, tiles);
+                grad_keys<T, kDim, kDrop, false, true, false>(a, out, place(), tid, tiles);
             }
         }
     } else {
         const uint32_t item = block - static_cast<uint32_t>(out.key_blocks);
-        const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows, kCausal>(a, item, true, out.q_splits, out.q_slots);
+        const Place w = place_of<QueryTiles<T, kDim, kSplitKeys>::kRows>(a, item, true, out.q_splits, out.q_slots);
         if (!w.any) return;
         if constexpr (kExactDelta<T, kCausal>) {
-            if (w.keys <= kExactStates) return grad_queries<T, kDim, kDrop, kSplitKeys, true, kCausal>(a, out, w, lds);
+            if (w.keys <= kExactStates) {
+                grad_queries<T, kDim, kDrop, kSplitKeys, true, false, false>(a, out, w, threadIdx.x, lds);
+                return;
+            }
         }
-        grad_queries<T, kDim, kDrop, kSplitKeys, false, kCausal>(a, out, w, lds);
+        grad_queries<T, kDim, kDrop, kSplitKeys, false, false, false>(a, out, w, threadIdx.x, lds);
     }
 }
 
@@ -842,21 +927,25 @@ struct Sum {
     const int32_t *ptr;
     int64_t rows, row;  // row = 0: nothing to do
     int splits;
+    const int32_t *pieces;  // causal: of each `dim` values, how many arrays hold them (one: the result is there)
+    int dim;
 };
 struct Sums {
     Sum job[3];
     int32_t n_struct;
 };
-template <class T>
+template <class T, bool kCausal>
 __global__ void __launch_bounds__(kThreads) k_add(Sums sums) {
     const int64_t step = int64_t(gridDim.x) * kThreads * 8;
     for (const Sum &j : sums.job) {
         const Span held = span_of(j.ptr[0], j.ptr[sums.n_struct], j.rows);
         const int64_t n = j.rows * j.row, end = held.end * j.row;
         for (int64_t i = held.begin * j.row + (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < end; i += step) {
+            const int splits = kCausal ? j.pieces[i / j.dim] : j.splits;
+            if (kCausal && splits == 1) continue;
             f32x8 v = load8(j.part + i);
 #pragma unroll 8
-            for (int s = 1; s < j.splits; ++s) v += load8(j.part + s * n + i);
+            for (int s = 1; s < splits; ++s) v += load8(j.part + s * n + i);
             store8(static_cast<T *>(j.out) + i, from_f32<T>(v));
         }
     }
@@ -867,8 +956,9 @@ constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
 struct Choice {
     bool split_keys;
     int q_splits, k_splits;
+    int piece;  // see Bwd
     int64_t q_slots, k_slots;
-    size_t part_q, part_k, delta, bytes;  // bytes of the partial sums, k for each of k and v, and of delta
+    size_t part_q, part_k, delta, q_pieces, k_pieces, bytes;  // bytes of the partial sums, k for each of k and v, and of more
 };
 
 // Splits of a walk of `walk` rows, so that none is longer than `share`, what a workgroup has if the
@@ -908,6 +998,9 @@ hipError_t backward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
     out.part_k = reinterpret_cast<float *>(ws + c.part_q);
     out.part_v = reinterpret_cast<float *>(ws + c.part_q + c.part_k);
     out.delta = reinterpret_cast<float *>(ws + c.part_q + 2 * c.part_k);
+    out.q_pieces = reinterpret_cast<int32_t *>(ws + c.part_q + 2 * c.part_k + c.delta);
+    out.k_pieces = reinterpret_cast<int32_t *>(ws + c.part_q + 2 * c.part_k + c.delta + c.q_pieces);
+    out.piece = c.piece;
     out.q_splits = c.q_splits, out.k_splits = c.k_splits, out.q_slots = c.q_slots, out.k_slots = c.k_slots;
     out.key_blocks = a.grad_k || a.grad_v ? c.k_slots * a.kv_heads * c.k_splits : 0;
     const int64_t blocks = out.key_blocks + (a.grad_q ? c.q_slots * a.kv_heads * c.q_splits : 0);
@@ -921,14 +1014,14 @@ hipError_t backward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
         launch<T, 128, kCausal>(a, c, out, blocks, stream);
     const int64_t q_row = a.grad_q && c.q_splits > 1 ? int64_t(a.heads) * a.dim : 0;
     const int64_t k_row = c.k_splits > 1 ? int64_t(a.kv_heads) * a.dim : 0;
-    const Sums sums = {{{out.part_q, a.grad_q, a.q_ptr, a.q_rows, q_row, c.q_splits},
-                        {out.part_k, a.grad_k, a.k_ptr, a.k_rows, a.grad_k ? k_row : 0, c.k_splits},
-                        {out.part_v, a.grad_v, a.k_ptr, a.k_rows, a.grad_v ? k_row : 0, c.k_splits}},
+    const Sums sums = {{{out.part_q, a.grad_q, a.q_ptr, a.q_rows, q_row, c.q_splits, out.q_pieces, a.dim},
+                        {out.part_k, a.grad_k, a.k_ptr, a.k_rows, a.grad_k ? k_row : 0, c.k_splits, out.k_pieces, a.dim},
+                        {out.part_v, a.grad_v, a.k_ptr, a.k_rows, a.grad_v ? k_row : 0, c.k_splits, out.k_pieces, a.dim}},
                        a.n_struct};
     const int64_t nq = a.q_rows * q_row, nk = a.grad_k || a.grad_v ? a.k_rows * k_row : 0;
     const int64_t most = nq > nk ? nq : nk, grid = (most / 8 + kThreads - 1) / kThreads;
     if (most)
-        k_add<T><<<dim3(static_cast<unsigned>(grid > 4096 ? 4096 : grid)), dim3(kThreads), 0, stream>>>(sums);
+        k_add<T, kCausal><<<dim3(static_cast<unsigned>(grid > 4096 ? 4096 : grid)), dim3(kThreads), 0, stream>>>(sums);
     return hipGetLastError();
 }
 

@@ -207,17 +207,26 @@ struct Place {
 // kCausal: the longest walks come first, those of the last query rows and of the first keys (an even
 // end: 4 x 1024 rows FIGORDER), and the key heads of a tile follow each other, so that with eight heads, or
 // four, an XCD's workgroups read one head's keys.
+// `even`: every walk has all its splits, which then follow each other, so that an XCD's workgroups read the same
+// part of the keys.  Else the first splits of all walks come first: some walks have fewer, and what does
+// not exist is spread over the XCDs.
 template <int kTile, bool kCausal = false>
-__device__ __forceinline__ Place place_of(const AttnArgs &a, uint32_t item, bool by_query, int splits, int64_t n_slots) {
+__device__ __forceinline__ Place place_of(const AttnArgs &a, uint32_t item, bool by_query, int splits, int64_t n_slots,
+                                          bool even = true) {
     Place p;
-    const uint32_t slots = static_cast<uint32_t>(n_slots), rest = item / static_cast<uint32_t>(splits);
-    p.split = static_cast<int>(item - rest * splits);
+    const uint32_t slots = static_cast<uint32_t>(n_slots);
     int64_t slot;
     if (kCausal) {
-        const uint32_t kv_heads = static_cast<uint32_t>(a.kv_heads), tile = rest / kv_heads;
+        const uint32_t kv_heads = static_cast<uint32_t>(a.kv_heads), walks = slots * kv_heads;
+        uint32_t rest = item / (even ? static_cast<uint32_t>(splits) : walks);
+        p.split = static_cast<int>(even ? item - rest * splits : rest);
+        rest = even ? rest : item - rest * walks;
+        const uint32_t tile = rest / kv_heads;
         p.kv_head = static_cast<int>(rest - tile * kv_heads);
         slot = by_query ? slots - 1 - tile : tile;
     } else {
+        const uint32_t rest = item / static_cast<uint32_t>(splits);
+        p.split = static_cast<int>(item - rest * splits);
         p.kv_head = static_cast<int>(rest / slots);
         slot = rest - p.kv_head * slots;
     }
@@ -294,6 +303,25 @@ __device__ __forceinline__ bool finite(const f32x16 (&sum)[kOut]) {
     }
     return fabsf(all[0]) < INFINITY;
 }
+
+// A kernel's arguments for a function that is not inlined, by LDS: `put` copies them there, `get` takes them out
+// again, the same for all lanes.  So walks that are seldom taken (with care) have registers of their own, and
+// the kernel's other walks are compiled as if they were not there.
+template <class A>
+struct Passed {
+    static constexpr int kWords = (sizeof(A) + 3) / 4;
+    uint32_t word[kWords];
+    // by one thread, with a barrier before and after
+    __device__ __forceinline__ void put(const A &a) { __builtin_memcpy(word, &a, sizeof a); }
+    __device__ __forceinline__ A get() const {
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __builtin_amdgcn_readfirstlane(word[i]);
+        A a;
+        __builtin_memcpy(&a, w, sizeof a);
+        return a;
+    }
+};
 
 }  // namespace readout
 }  // namespace oeq

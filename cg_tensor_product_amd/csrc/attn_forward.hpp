@@ -65,6 +65,10 @@ __device__ __forceinline__ bool any_wave(bool v) {
 struct Partial {
     float *out;  // [split][query row, head][dim], normalised
     float *lse;  // [split][query row, head], in powers of two
+    // causal: walks of different lengths are cut into pieces of about this many tiles, at most `splits` of them (0:
+    // all into `splits`); [query row, head]: into how many
+    int piece;
+    int32_t *pieces;
 };
 
 // f(i, v) with a lane's results of a 32 x 32 block as eight consecutive rows of it from 8 i on (the
@@ -87,19 +91,41 @@ __device__ __forceinline__ void each_eight(f32x16 o, int half, F &&f) {
     }
 }
 
+// The waves' rows (or keys) of a workgroup.  kCausal: walks grow from wave to wave, and the workgroups of a compute
+// unit, 256 blocks apart, take them in turn forwards and backwards, so that no SIMD has all the long ones.
+template <bool kCausal>
+__device__ __forceinline__ int part_of(int wave) {
+    return kCausal && (blockIdx.x >> 8 & 1) ? kWaves - 1 - wave : wave;
+}
+
+// Workgroups that a compute unit is to hold of the causal kernels, where registers allow it.
+template <class T, int kDim>
+constexpr int kHeld = sizeof(T) == 4 ? 1 : kDim <= 32 ? 3 : 2;
+
+// In pairs: a chain of sixteen additions would be waited for.
+__device__ __forceinline__ float sum_of(f32x16 v) {
+#pragma unroll
+    for (int n = 8; n > 0; n >>= 1) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] += v[n + i];
+    }
+    return v[0];
+}
+
 template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kCausal>
-__global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k_forward(AttnArgs a, int splits, int64_t slots, Partial partial) {
+__global__ void __launch_bounds__(kThreads, (kCausal ? kHeld<T, kDim> : 1))
+    k_forward(AttnArgs a, int splits, int64_t slots, Partial partial) {
     using C = Tiles<T, kDim, kSplitKeys>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32, kSub = kKeys / 32;
     __shared__ __attribute__((aligned(16))) char lds[C::kBytes];
-    const Place w = place_of<C::kRows, kCausal>(a, blockIdx.x, true, splits, slots);
+    const Place w = place_of<C::kRows, kCausal>(a, blockIdx.x, true, splits, slots, partial.piece == 0);
     if (!w.any) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
     const int thread = kSplitKeys ? lane : threadIdx.x;
     T *k_tile = reinterpret_cast<T *>(lds) + (kSplitKeys ? wave * 2 * C::kTile : 0), *v_tile = k_tile + C::kTile;
 
     // this lane's query row
-    const int r = w.first + (kSplitKeys ? 0 : wave * 32) + (lane & 31);
+    const int base = w.first + (kSplitKeys ? 0 : part_of<kCausal>(wave) * 32), r = base + (lane & 31);
     const bool row_ok = r < w.rows;
     const int64_t q_row = w.q_begin + (row_ok ? r / a.share : 0);
     const int head = w.kv_head * a.share + (row_ok ? r % a.share : 0);
@@ -115,14 +141,25 @@ __global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k
     // last rows do
     int keys = w.keys, limit = 0, wave_first = 0, wave_last = 0;
     if (kCausal) {
-        const int off = causal_offset(a, w), most = w.rows - 1, base = w.first + (kSplitKeys ? 0 : wave * 32);
+        const int off = causal_offset(a, w), most = w.rows - 1;
         keys = max(0, min(keys, min(w.first + C::kRows - 1, most) / a.share + off + 1));
         limit = min(r, most) / a.share + off;
         wave_first = __builtin_amdgcn_readfirstlane(min(base, most) / a.share + off);
         wave_last = __builtin_amdgcn_readfirstlane(min(base + 31, most) / a.share + off);
     }
     // this workgroup's keys, in whole tiles
-    const int n_tiles = (keys + kKeys - 1) / kKeys, per = (n_tiles + splits - 1) / splits;
+    const int n_tiles = (keys + kKeys - 1) / kKeys;
+    int pieces = splits;
+    if (kCausal && partial.piece) {
+        pieces = max(1, min(splits, (n_tiles + partial.piece - 1) / partial.piece));
+        if (w.split >= pieces) return;
+        if (w.split == 0 && threadIdx.x < C::kRows) {
+            const int row = w.first + static_cast<int>(threadIdx.x);
+            if (row < w.rows)
+                partial.pieces[(w.q_begin + row / a.share) * a.heads + w.kv_head * a.share + row % a.share] = pieces;
+        }
+    }
+    const int per = (n_tiles + pieces - 1) / pieces;
     const int t_end = min(n_tiles, (w.split + 1) * per), t_step = kSplitKeys ? kWaves : 1;
     const T *k_base = static_cast<const T *>(a.k) + w.k_begin * a.k_row + w.kv_head * a.k_head;
     const T *v_base = static_cast<const T *>(a.v) + w.k_begin * a.v_row + w.kv_head * a.v_head;
@@ -143,114 +180,139 @@ __global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k
             qf[s] = row_ok && d < a.dim && t < t_end ? *reinterpret_cast<const vec8<T> *>(q + d) : vec8<T>(T(0.f));
         }
     }
-    for (bool care = false;; care = true) {
-        for (; t < t_end; t += t_step) {
-            if (kSplitKeys) wave_sync();
-            const uint64_t valid = in.store(k_tile, v_tile);
-            if (kSplitKeys) wave_sync(); else __syncthreads();
-            const int k0 = t * kKeys;
-            in.fetch(a, k_base, v_base, mask, keys, min(t + t_step, t_end - 1));  // at the end, again the last
-            const auto turn = [&]() {
-                // shared tiles have two buffers: one barrier a tile, since no wave is a whole tile ahead
-                if (!kSplitKeys) {
-                    k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
-                    v_tile = k_tile + C::kTile;
-                }
-            };
-            if (kCausal && k0 > wave_last) {  // no row of this wave sees any of it
-                turn();
-                continue;
+    for (; t < t_end; t += t_step) {
+        if (kSplitKeys) wave_sync();
+        const uint64_t valid = in.store(k_tile, v_tile);
+        if (kSplitKeys) wave_sync(); else __syncthreads();
+        const int k0 = t * kKeys;
+        in.fetch(a, k_base, v_base, mask, keys, min(t + t_step, t_end - 1));  // at the end, again the last
+        const auto turn = [&]() {
+            // shared tiles have two buffers: one barrier a tile, since no wave is a whole tile ahead
+            if (!kSplitKeys) {
+                k_tile = reinterpret_cast<T *>(lds) + (buffer ^= 1) * 2 * C::kTile;
+                v_tile = k_tile + C::kTile;
             }
+        };
+        if (kCausal && k0 > wave_last) {  // no row of this wave sees any of it
+            turn();
+            continue;
+        }
 
-            f32x16 s[kSub];
+        f32x16 s[kSub];
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                s[u] = f32x16{};
-                const int row = 32 * u + permuted_row(lane & 31);
+        for (int u = 0; u < kSub; ++u) {
+            s[u] = f32x16{};
+            const int row = 32 * u + permuted_row(lane & 31);
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) s[u] = mma(s[u], row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
+            for (int i = 0; i < kSteps; ++i) s[u] = mma(s[u], row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
+        }
+        uint64_t used_keys = valid;
+        const bool cut = kCausal && k0 + kKeys - 1 > wave_first;  // some row of the wave sees only a part
+        if (cut) used_keys &= low_bits(limit - k0 + 1);
+        if (valid != ~0ull || cut) {
+            rare();
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+                each_score(static_cast<uint32_t>(used_keys >> (32 * u)), half,
+                           [&](int i, bool used) { s[u][i] = used ? s[u][i] : -INFINITY; });
+        }
+        float high = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) high = fmaxf(high, s[u][i]);
+        }
+        high = max_halves(high);
+        // top = -inf (nothing seen yet) always moves on; a row that has seen nothing stays there
+        if (__any((high - top) * c > kLag || (top == -INFINITY && high > -INFINITY))) {
+            rare();
+            const float now = fmaxf(top, high);
+            const float scale = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((top - now) * c);
+            sum *= scale;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) o[d] *= scale;
+            top = now;
+        }
+        const float shift = top == -INFINITY ? 0.f : top * c;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            vec8<T> p[2];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -shift));
+                if (!kCausal) sum += e;
+                s[u][i] = e;
             }
-            uint64_t used_keys = valid;
-            const bool cut = kCausal && k0 + kKeys - 1 > wave_first;  // some row of the wave sees only a part
-            if (cut) used_keys &= low_bits(limit - k0 + 1);
-            if (valid != ~0ull || cut) {
-                rare();
+            if (kCausal) sum += sum_of(s[u]);
 #pragma unroll
-                for (int u = 0; u < kSub; ++u)
-                    each_score(static_cast<uint32_t>(used_keys >> (32 * u)), half,
-                               [&](int i, bool used) { s[u][i] = used ? s[u][i] : -INFINITY; });
+            for (int h = 0; h < 2; ++h) {
+                f32x8 e;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = s[u][8 * h + j];
+                if (kDrop) {
+                    const uint32_t keep = keep_bits(g, (k0 + 32 * u + 16 * h) / 8 + half, drop_row, a.threshold);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = (keep >> j & 1) ? e[j] : 0.f;
+                }
+                // 16-bit types round p once, as the product takes it: with that out has 1.3 to 1.4 times the
+                // error of rounding it alone; the rest as a second term would be half as many products more.
+                p[h] = from_f32<T>(e);
             }
-            float high = s[0][0];
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) high = fmaxf(high, s[u][i]);
+            for (int d = 0; d < kOut; ++d) {
+                o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u, 32 * d, lane), p[0]);
+                o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u + 16, 32 * d, lane), p[1]);
             }
-            high = max_halves(high);
-            // top = -inf (nothing seen yet) always moves on; a row that has seen nothing stays there
-            if (__any((high - top) * c > kLag || (top == -INFINITY && high > -INFINITY))) {
-                rare();
-                const float now = fmaxf(top, high);
-                const float scale = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((top - now) * c);
-                sum *= scale;
+        }
+        turn();
+    }
+    if constexpr (kCausal) {
+        if (any_wave(__any(row_ok && !finite(o)))) {
+            rare();
+            // again with care: the maximum and the sum are known, tiles are neither read ahead nor taken together
 #pragma unroll
-                for (int d = 0; d < kOut; ++d) o[d] *= scale;
-                top = now;
-            }
+            for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
             const float shift = top == -INFINITY ? 0.f : top * c;
+#pragma unroll 1
+            for (t = t_begin; t < t_end; t += t_step) {
+                in.fetch(a, k_base, v_base, mask, keys, t);
+                if (kSplitKeys) wave_sync(); else __syncthreads();
+                const uint64_t valid = in.store(k_tile, v_tile);
+                if (kSplitKeys) wave_sync(); else __syncthreads();
+                const int k0 = t * kKeys;
+                if (k0 > wave_last) continue;
+#pragma unroll 1
+                for (int u = 0; u < kSub; ++u) {
+                    const T *k_sub = k_tile + 32 * u * kRow, *v_sub = v_tile + 32 * u * kRow;
+                    const int first = k0 + 32 * u;
+                    const uint32_t used = static_cast<uint32_t>(valid >> (32 * u) & low_bits(limit - first + 1));
+                    const bool cut = first + 31 > wave_first;
+                    f32x16 s = {};
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                vec8<T> p[2];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -shift));
-                    sum += e;
-                    s[u][i] = e;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f32x8 e;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) e[j] = s[u][8 * h + j];
-                    if (kDrop) {
-                        const uint32_t keep = keep_bits(g, (k0 + 32 * u + 16 * h) / 8 + half, drop_row, a.threshold);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) e[j] = (keep >> j & 1) ? e[j] : 0.f;
-                    }
-                    // 16-bit types round p once, as the product takes it: with that out has 1.3 to 1.4 times the
-                    // error of rounding it alone; the rest as a second term would be half as many products more.
-                    p[h] = from_f32<T>(e);
-                }
-                const bool careful = kCausal && care && cut;
-#pragma unroll
-                for (int d = 0; d < kOut; ++d) {
+                    for (int i = 0; i < kSteps; ++i)
+                        s = mma(s, row_operand(k_sub, kRow, permuted_row(lane & 31), 16 * i, half), qf[i]);
+                    each_score(used, half, [&](int i, bool in) {
+                        s[i] = in ? __builtin_amdgcn_exp2f(fmaf(s[i], c, -shift)) : 0.f;
+                    });
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        vec8<T> v = column_operand(v_tile, kRow, 32 * u + 16 * h, 32 * d, lane);
-                        if (careful) {
-                            rare();
-                            v = finite_only<T>(v);
+                        f32x8 e;
+                        const uint32_t keep =
+                            kDrop ? keep_bits(g, (first + 16 * h) / 8 + half, drop_row, a.threshold) : 0xFFu;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) e[j] = (keep >> j & 1) ? s[8 * h + j] : 0.f;
+                        const vec8<T> p = from_f32<T>(e);
+#pragma unroll
+                        for (int d = 0; d < kOut; ++d) {
+                            vec8<T> v = column_operand(v_sub, kRow, 16 * h, 32 * d, lane);
+                            if (cut) v = finite_only<T>(v);
+                            o[d] = mma(o[d], v, p);
                         }
-                        o[d] = mma(o[d], v, p[h]);
                     }
-                }
-                if (careful) {
-                    rare();
-                    add_others<false>(o, v_tile + 32 * u * kRow, kRow, static_cast<uint32_t>(used_keys >> (32 * u)), half);
+                    if (cut) add_others<false>(o, v_sub, kRow, used, half);
                 }
             }
-            turn();
         }
-        if constexpr (!kCausal) break;
-        if (care) break;
-        const bool lost = __any(row_ok && !finite(o));
-        if (kSplitKeys ? !lost : !any_wave(lost)) break;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
-        top = -INFINITY;
-        sum = 0.f;
-        t = t_begin;
-        if (t < t_end) in.fetch(a, k_base, v_base, mask, keys, t);
     }
     sum = sum_halves(sum);
 
@@ -259,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k
         if (!row_ok) return;
         const float lse2 = sum > 0.f || sum != sum ? top * c + __builtin_amdgcn_logf(sum) : -INFINITY;
         const float norm = sum > 0.f || sum != sum ? a.keep_scale / sum : 0.f;
-        if (splits > 1) {
+        if (pieces > 1) {
             const int64_t to = int64_t(w.split) * a.q_rows * a.heads + at;
             if (half == 0) partial.lse[to] = lse2;
 #pragma unroll
@@ -317,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k
     const int64_t q_out = (w.q_begin + row / a.share) * a.heads + w.kv_head * a.share + row % a.share;
     const int64_t to = int64_t(w.split) * a.q_rows * a.heads + q_out;
     if (jc == 0) {
-        if (splits > 1)
+        if (pieces > 1)
             partial.lse[to] = lse2;
         else
             a.lse[q_out] = lse2 * kLn2;
@@ -331,16 +393,17 @@ __global__ void __launch_bounds__(kThreads, kCausal && sizeof(T) == 2 ? 2 : 1) k
             for (int j = 0; j < 8; ++j) v[j] += from[j] * weight[i];
         }
         v *= norm;
-        if (splits > 1)
+        if (pieces > 1)
             store8(partial.out + to * a.dim + col, v);
         else
             store8(static_cast<T *>(a.out) + q_out * a.dim + col, from_f32<T>(v));
     }
+    return;
 }
 
 // Joins the splits: eight columns of one (query row, head) a thread, kLanes threads for the
 // columns times kGroups that share the splits.
-template <class T, int kLanes, int kGroups>
+template <class T, int kLanes, int kGroups, bool kCausal>
 __global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Partial partial) {
     constexpr int kAhead = 4, kRow = kLanes * kGroups;
     const int64_t n = a.q_rows * a.heads, at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kRow;
@@ -349,6 +412,10 @@ __global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Parti
     // end here: the exchanges below stay within one.
     const Span held = span_of(a.q_ptr[0], a.q_ptr[a.n_struct], a.q_rows);
     if (at < held.begin * a.heads || at >= held.end * a.heads) return;
+    if (kCausal && partial.piece) {
+        splits = partial.pieces[at];
+        if (splits == 1) return;  // written by its walk
+    }
     float most = -INFINITY, total = 0.f, bad = 0.f;
     f32x8 v = {};
     for (int first = group; first < splits; first += kGroups * kAhead) {
@@ -404,7 +471,7 @@ constexpr size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Choice {
     bool split_keys;
-    int splits;
+    int splits, piece;  // piece: see Partial
     int64_t slots, blocks;
 };
 
@@ -418,7 +485,7 @@ void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStrea
     // without rows in it, so the bound is a rough one: at 560 the two places win (4 x 384 rows: 27 us for 30), at
     // 608 and 640 the three (4 x 1152: 44 for 53), and at 576 either does (4 x 512: 26 for 29 with two;
     // 8 x 512: 43 for 49 with three).
-    const unsigned spare = sizeof(T) == 2 && kDim == 64 && c.blocks <= 576 ? 20480 : 0;
+    const unsigned spare = sizeof(T) == 2 && kDim == 64 && c.blocks <= 576 && c.piece == 0 ? 20480 : 0;
     if (c.split_keys)
         k_forward<T, kDim, kDrop, true, kCausal><<<grid, threads, 0, stream>>>(a, c.splits, c.slots, partial);
     else
@@ -436,6 +503,9 @@ void launch(const AttnArgs &a, const Choice &c, const Partial &partial, hipStrea
 inline size_t partial_out(const AttnArgs &a, const Choice &c) {
     return up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * a.dim * sizeof(float));
 }
+inline size_t partial_lse(const AttnArgs &a, const Choice &c) {
+    return up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * sizeof(float));
+}
 
 template <class T, bool kCausal>
 hipError_t forward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
@@ -443,6 +513,8 @@ hipError_t forward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
     if (c.splits > 1) {
         partial.out = static_cast<float *>(a.workspace);
         partial.lse = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + partial_out(a, c));
+        partial.pieces = reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + partial_out(a, c) + partial_lse(a, c));
+        partial.piece = c.piece;
     }
     if (a.dim <= 32)
         launch<T, 32, kCausal>(a, c, partial, stream);
@@ -456,13 +528,15 @@ hipError_t forward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
         const int64_t n = a.q_rows * a.heads;
         const auto join = [&](auto lanes) {
             constexpr int kLanes = decltype(lanes)::value;
-            // many splits are shared by the threads of a wave, since they come with few rows
-            const int row = c.splits > 4 ? 64 : kLanes;
+            // many splits are shared by the threads of a wave, since they come with few rows (not where walks have
+            // as many as their length asks for)
+            const bool share = c.splits > 4 && c.piece == 0;
+            const int row = share ? 64 : kLanes;
             const dim3 grid(static_cast<unsigned>((n * row + kThreads - 1) / kThreads));
-            if (c.splits > 4)
-                k_join<T, kLanes, 64 / kLanes><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
+            if (share)
+                k_join<T, kLanes, 64 / kLanes, kCausal><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
             else
-                k_join<T, kLanes, 1><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
+                k_join<T, kLanes, 1, kCausal><<<grid, dim3(kThreads), 0, stream>>>(a, c.splits, partial);
         };
         if (a.dim <= 32)
             join(std::integral_constant<int, 4>());
@@ -474,9 +548,9 @@ hipError_t forward(const AttnArgs &a, const Choice &c, hipStream_t stream) {
     return hipGetLastError();
 }
 
-inline size_t forward_workspace(const AttnArgs &a, const Choice &c) {
+inline size_t forward_workspace(const AttnArgs &a, const Choice &c, bool causal) {
     if (c.splits == 1) return 0;
-    return partial_out(a, c) + up(static_cast<size_t>(c.splits) * a.q_rows * a.heads * sizeof(float));
+    return partial_out(a, c) + partial_lse(a, c) + (causal ? up(static_cast<size_t>(a.q_rows) * a.heads * 4) : 0);
 }
 
 }  // namespace

@@ -15,21 +15,29 @@ namespace {
 
 inline Choice choose(const AttnArgs &a) {
     Choice c{};
-    // Twice the workgroups the chip holds at once: walks half as long even out better than their
-    // partial sums cost (bf16, D = 64, 4 structures of 1024 query rows and 2048 states: 111 us,
-    // 135 with walks of one round).
-    const int64_t fill = 1024;
-    c.split_keys = a.q_rows * a.share <= 32 * int64_t(a.n_struct);
+    const int64_t rows = a.q_rows * a.share;
+    c.split_keys = rows <= 32 * int64_t(a.n_struct);
     c.q_slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
     c.k_slots = tile_slots(a.k_rows, a.n_struct, 1, kKeyTile);
-    const int64_t keys = a.k_rows / a.n_struct, rows = a.q_rows * a.share / a.n_struct;
-    const int64_t share = (c.q_slots * a.kv_heads * keys + c.k_slots * a.kv_heads * rows) / fill;
-    c.q_splits = splits_of(keys, share);
-    c.k_splits = splits_of(rows, share);
+    // Pieces as in the forward, over both roles; a tile of either walk is about the same work.
+    const int64_t n = rows / a.n_struct, m = a.k_rows / a.n_struct;
+    const int64_t q_walk = (m > n / a.share ? m - n / a.share / 2 : m / 2) / 32 + 1;
+    const int64_t k_walk = (m > n / a.share ? n - n * (n / a.share) / (2 * m) : n / 2) / kRowTile + 1;
+    const int64_t total = ((rows / (c.split_keys ? 32 : 128) + 1) * q_walk + (a.k_rows / kKeyTile + 1) * k_walk) * a.kv_heads;
+    const int64_t fill = 768;
+    c.piece = static_cast<int>(std::max<int64_t>(8, (total + fill - 1) / fill));
+    const auto splits = [&](int64_t longest) {
+        const int64_t most = longest <= c.piece ? 1 : ((a.n_struct > 1 ? 2 : 1) * longest + c.piece - 1) / c.piece;
+        return static_cast<int>(most > 16 ? 16 : most);
+    };
+    c.q_splits = splits(m / 32 + 1);
+    c.k_splits = splits(n / kRowTile + 1);
     c.part_q = c.q_splits > 1 ? up(static_cast<size_t>(c.q_splits) * a.q_rows * a.heads * a.dim * 4) : 0;
     c.part_k = c.k_splits > 1 ? up(static_cast<size_t>(c.k_splits) * a.k_rows * a.kv_heads * a.dim * 4) : 0;
     c.delta = up(static_cast<size_t>(a.q_rows) * a.heads * 4);
-    c.bytes = c.part_q + 2 * c.part_k + c.delta;
+    c.q_pieces = c.q_splits > 1 ? c.delta : 0;
+    c.k_pieces = c.k_splits > 1 ? up(static_cast<size_t>(a.k_rows) * a.kv_heads * 4) : 0;
+    c.bytes = c.part_q + 2 * c.part_k + c.delta + c.q_pieces + c.k_pieces;
     return c;
 }
 

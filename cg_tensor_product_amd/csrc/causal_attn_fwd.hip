@@ -1,4 +1,6 @@
 // Causal attention forward (attn_forward.hpp): a query row sees the states up to its own place.
+#include <algorithm>
+
 #include "attn_forward.hpp"
 
 namespace oeq {
@@ -7,26 +9,34 @@ namespace readout {
 namespace {
 
 Choice choose(const AttnArgs &a) {
-    Choice c;
+    Choice c{};
     const int64_t rows = a.q_rows * a.share;
     c.split_keys = rows <= 32 * int64_t(a.n_struct);
     c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
-    // Splits until the workgroups fill the chip about once (256 compute units; four workgroups each
-    // at D <= 32, else two).  4 structures of 1024 query rows and 2048 states, 8 heads over 4:
-    // bf16, D = 64 takes 36 us with 512 workgroups, 49 with 768 and 45 with 1024; D = 32 takes
-    // 39, 37 and 31 us; fp32, D = 128 takes 303, 400 and 324 us.
-    const int64_t fill = 256 * (a.dim <= 32 ? 4 : 2);
-    const int64_t base = c.slots * a.kv_heads, most = a.k_rows / a.n_struct / 256;  // 256 keys a split at least
-    int64_t splits = (fill + base / 2) / base;
-    splits = splits > most ? most : splits;
-    c.splits = static_cast<int>(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    const int64_t base = c.slots * a.kv_heads, tile = c.split_keys ? 32 : 64;
+    // Tiles of all walks, for sequences of the average lengths, and of the longest of these.  A piece is what a
+    // workgroup has if the work is spread evenly over the chip, 256 keys at least; sequences of twice the
+    // average length are still cut so, longer ones into longer pieces.
+    const int64_t n = a.q_rows / a.n_struct, m = a.k_rows / a.n_struct;
+    if (m >= 4 * n) {  // the walks of a sequence are alike: split as in the cross attention
+        const int64_t most = m / 256, blocks = 256 * (a.dim <= 32 ? 4 : 2), splits = std::min((blocks + base / 2) / base, most);
+        c.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(splits, 64)));
+        c.blocks = base * c.splits;
+        return c;
+    }
+    const int64_t longest = m / tile + 1, walk = (m > n ? m - n / 2 : m / 2) / tile + 1;
+    const int64_t total = (rows / (c.split_keys ? 32 : 128) + 1) * a.kv_heads * walk, fill = 256 * (a.dim <= 32 ? 3 : 2);
+    c.piece = static_cast<int>(std::max<int64_t>(256 / tile, (total + fill - 1) / fill));
+    const int64_t splits = longest <= c.piece ? 1 : ((a.n_struct > 1 ? 2 : 1) * longest + c.piece - 1) / c.piece;
+    c.splits = static_cast<int>(splits > 16 ? 16 : splits);
+    if (c.splits == 1) c.piece = 0;
     c.blocks = base * c.splits;
     return c;
 }
 
 }  // namespace
 
-size_t causal_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) { return forward_workspace(a, choose(a)); }
+size_t causal_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) { return forward_workspace(a, choose(a), true); }
 
 int64_t causal_attn_fwd_blocks(oeq_dtype, const AttnArgs &a) { return choose(a).blocks; }
 

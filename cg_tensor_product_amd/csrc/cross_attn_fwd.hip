@@ -7,7 +7,7 @@ namespace readout {
 namespace {
 
 Choice choose(const AttnArgs &a) {
-    Choice c;
+    Choice c{};
     const int64_t rows = a.q_rows * a.share;
     c.split_keys = rows <= 32 * int64_t(a.n_struct);
     c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
@@ -26,7 +26,7 @@ Choice choose(const AttnArgs &a) {
 
 }  // namespace
 
-size_t cross_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) { return forward_workspace(a, choose(a)); }
+size_t cross_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) { return forward_workspace(a, choose(a), false); }
 
 int64_t cross_attn_fwd_blocks(oeq_dtype, const AttnArgs &a) { return choose(a).blocks; }
 
