@@ -206,6 +206,9 @@ __global__ void __launch_bounds__(kThreads, (kCausal ? kHeld<T, kDim> : 1))
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) s[u] = mma(s[u], row_operand(k_tile, kRow, row, 16 * i, half), qf[i]);
         }
+        // Between the products a wave goes first: with two waves on a SIMD, one's exponentials then run beside the
+        // other's products (2 x 4096 rows, 16 heads over 4, D = 128, fp16: 181 -> 172 us)
+        if (kCausal) __builtin_amdgcn_s_setprio(1);
         uint64_t used_keys = valid;
         const bool cut = kCausal && k0 + kKeys - 1 > wave_first;  // some row of the wave sees only a part
         if (cut) used_keys &= low_bits(limit - k0 + 1);
@@ -264,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, (kCausal ? kHeld<T, kDim> : 1))
                 o[d] = mma(o[d], column_operand(v_tile, kRow, 32 * u + 16, 32 * d, lane), p[1]);
             }
         }
+        if (kCausal) __builtin_amdgcn_s_setprio(0);
         turn();
     }
     if constexpr (kCausal) {

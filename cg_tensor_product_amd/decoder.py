@@ -121,16 +121,14 @@ def _rms_fwd(x, weight, residual, eps, out, total, out_dtype):
     else:
         total = x
     if out is None:
-        out, ld_o = torch.empty((rows, cols), dtype=out_dtype, device=x.device), cols
+        out, ld_o = x.new_empty((rows, cols), dtype=out_dtype), cols
     else:
         _typed(out, out_dtype, dev, "out")
         if out.shape != (rows, cols):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, cols)}")
         ld_o = _row_stride(out, "out")
-    if out_dtype is _E4M3:
-        scale, rstd = torch.empty((2, rows), dtype=_F32, device=x.device).unbind(0)
-    else:
-        scale, rstd = None, torch.empty(rows, dtype=_F32, device=x.device)
+    rstd = x.new_empty(rows, dtype=_F32)
+    scale = x.new_empty(rows, dtype=_F32) if out_dtype is _E4M3 else None
     st = lib().oeq_rms_norm_fwd(code, rows, cols, eps, x.data_ptr(), ld, res, ld_r, w, at, ld_s, out.data_ptr(), ld_o,
                                 None if scale is None else scale.data_ptr(), rstd.data_ptr(), _raw_stream(dev))
     if st:
@@ -174,7 +172,7 @@ def oeq_rms_norm_bwd(sum, rstd, grad_out, weight=None, grad_sum=None, need=("x",
         else:
             gx, ld_x = out, _like(out, sum, dev, "grad_x")
     if "weight" in need:
-        gw = torch.empty(cols, dtype=_F32, device=sum.device)
+        gw = sum.new_empty(cols, dtype=_F32)
         keep, ws, nbytes = _scratch(oeq_rms_norm_workspace_size(rows, cols), workspace, sum.device)
     st = lib().oeq_rms_norm_bwd(code, rows, cols, sum.data_ptr(), ld, w, rs, grad_out.data_ptr(), ld_g, gs, ld_gs,
                                 None if gx is None else gx.data_ptr(), ld_x, None if gw is None else gw.data_ptr(), ws,

@@ -1,6 +1,6 @@
 """A readout of whole structures on top of the convolution, trained end to end.
 
-    node features -> oeq_tp_conv_fwd_pos -> the scalar block of the rows, in place
+    species -> oeq_embedding_fwd -> node features -> oeq_tp_conv_fwd_pos -> the scalar block of the rows, in place
       -> oeq_group_norm_fwd (per structure, SiLU) -> keys and values (one dense product)
       -> oeq_cross_attn_fwd from a few learned query tokens to each structure's atoms
       -> oeq_dropout_fwd onto the tokens -> one number per structure
@@ -64,7 +64,7 @@ def forward(plan, model, batch, p_drop, rng):
     """Predictions [structures] and what the backward needs."""
     s = {}
     structures = batch["target"].shape[0]
-    s["x"] = model["embed"][batch["species"]]
+    s["x"] = oeq.oeq_embedding_fwd(model["embed"], batch["species"])
     s["W"] = model["edge"].expand(batch["src"].shape[0], -1, -1).contiguous()
     s["rows"] = oeq.oeq_tp_conv_fwd_pos(plan, batch["rowptr"], batch["src"], s["x"], batch["pos"], s["W"])
     # the first block of a row is its CHANNELS scalars: normalised where they are
@@ -100,7 +100,7 @@ def backward(plan, model, batch, s, grad, p_drop, rng):
         model["norm_weight"], model["norm_bias"], act="silu", out=grad_rows[:, :CHANNELS])
     gx, g_pos, gW = oeq.oeq_tp_conv_bwd_pos(plan, batch["rowptr"], batch["src"], s["x"], batch["pos"], s["W"],
                                             grad_rows)
-    g["embed"] = torch.zeros_like(model["embed"]).index_add_(0, batch["species"], gx)
+    g["embed"] = oeq.oeq_embedding_bwd(batch["species"], gx, SPECIES)
     g["edge"] = gW.sum(0, keepdim=True)
     return g, g_pos
 
