@@ -941,7 +941,8 @@ __global__ void __launch_bounds__(kThreads) k_add(Sums sums) {
         const Span held = span_of(j.ptr[0], j.ptr[sums.n_struct], j.rows);
         const int64_t n = j.rows * j.row, end = held.end * j.row;
         for (int64_t i = held.begin * j.row + (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < end; i += step) {
-            const int splits = kCausal ? j.pieces[i / j.dim] : j.splits;
+            // (as in the forward, a count that was not written is cut to the workspace)
+            const int splits = kCausal ? max(1, min(j.pieces[i / j.dim], j.splits)) : j.splits;
             if (kCausal && splits == 1) continue;
             f32x8 v = load8(j.part + i);
 #pragma unroll 8

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads) k_join(AttnArgs a, int splits, Parti
     const Span held = span_of(a.q_ptr[0], a.q_ptr[a.n_struct], a.q_rows);
     if (at < held.begin * a.heads || at >= held.end * a.heads) return;
     if (kCausal && partial.piece) {
-        splits = partial.pieces[at];
+        // (rows that a row pointer which decreases leaves out have no count: any, within the workspace)
+        splits = max(1, min(partial.pieces[at], splits));
         if (splits == 1) return;  // written by its walk
     }
     float most = -INFINITY, total = 0.f, bad = 0.f;

@@ -37,6 +37,8 @@ CASES = {
     "dim_80": ([100, 37], None, 4, 2, 80),
     "dim_104": ([140], [150], 2, 1, 104),
     "long": ([700], None, 1, 1, 32),
+    "tokens_of_wide_heads": ([1, 2], [300, 20], 2, 1, 128),
+    "ragged": ([900, 3, 40, 260], None, 2, 1, 64),
     "long_chunk": ([90], [1500], 2, 1, 96),
 }
 
@@ -392,6 +394,41 @@ def test_gradients_are_differences_of_the_forward():
         ends = [value(*(t + s * d if j == i else t for j, t in enumerate(args))) for s in (1e-2, -1e-2)]
         change = (ends[0] - ends[1]) / 2e-2
         assert abs(change - float((got[name].double() * d.double()).sum())) <= 1e-2 * float(got[name].norm()) + 6e-2
+
+
+@pytest.mark.parametrize("q_ptr,k_ptr", [([0, 90, 20, 130], [0, 90, 20, 130]), ([0, 400, 130], [0, -5, 130]),
+                                         ([0, 1 << 30, 1 << 30], [0, 64, 130]), ([130, 130, 0], [0, 0, 130])])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_row_pointers_that_are_not_row_pointers_stay_in_the_tensors(kind, q_ptr, k_ptr):
+    # the results mean nothing, but guard rows around every tensor stay as they are and the calls end
+    whole = torch.full((5, 330, 2, 32), 0.5, device="cuda").to(TYPES[kind])
+    q, k, v, g, out = (t[100:230] for t in whole)
+    grads = tuple(torch.full((330, 2, 32), 0.5, device="cuda").to(TYPES[kind]) for _ in range(3))
+    lse = torch.full((330, 2), 0.5, device="cuda")
+    args = (q, k, v, index(q_ptr), index(k_ptr))
+    oeq.oeq_causal_attn_fwd(*args, out=out, lse=lse[100:230])
+    oeq.oeq_causal_attn_bwd(*args, out, lse[100:230], g, grads=tuple(t[100:230] for t in grads))
+    torch.cuda.synchronize()
+    for t in (*whole, *grads, lse):
+        assert torch.all(t[:100] == 0.5) and torch.all(t[230:] == 0.5)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_a_cache_past_32_bit_offsets(kind):
+    # 2.2 G elements of keys; the second sequence stands at their end
+    n, used = (1 << 32) // (2 * 512) + 70000, 300
+    k, v = (torch.zeros((n, 4, 128), dtype=TYPES[kind], device="cuda") for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(TYPES[kind])  # noqa: E731
+    k[n - 400:n - 100], v[n - 400:n - 100] = rand(used, 4, 128), rand(used, 4, 128)
+    v[n - 100:] = float("nan")  # spare rows
+    q = rand(5, 8, 128)
+    out, lse = oeq.oeq_causal_attn_fwd(q, k, v, index([0, 2, 5]), index([0, n - 400, n]), k_len=index([7, used]))
+    small = oeq.oeq_causal_attn_fwd(q[2:], k[n - 400:n - 100].clone(), v[n - 400:n - 100].clone(), index([0, 3]),
+                                    index([0, used]))
+    close(out[2:], small[0], kind, "out")
+    assert rel_l2(host(lse[2:]), host(small[1])) <= RTOL["f32"]
+    assert torch.all(out[:2] == 0)  # of seven states of zeros
 
 
 def test_what_the_binding_refuses():

@@ -23,6 +23,8 @@ CASES = {
     "molecule": (89, 128, 56, 2.0, 0.0),
     "odd_columns": (7, 13, 300, 1.0, 0.1),
     "no_rows": (5, 24, 0, 1.0, 0.0),
+    "no_rows_of_a_long_table": (300, 24, 0, 1.0, 0.0),
+    "all_absent_of_a_long_table": (300, 24, 5000, 1.0, 1.0),
     "all_absent": (6, 16, 40, 1.0, 1.0),
     "one_row_table": (1, 40, 1000, 1.0, 0.0),
     "one_sorting_group": (700, 72, 4096, 2.0, 0.05),
