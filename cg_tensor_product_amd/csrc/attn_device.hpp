@@ -204,9 +204,10 @@ struct Place {
     bool any;
 };
 
-// kCausal: the longest walks come first, those of the last query rows and of the first keys (an even
-// end: 4 x 1024 rows FIGORDER), and the key heads of a tile follow each other, so that with eight heads, or
-// four, an XCD's workgroups read one head's keys.
+// kCausal: the longest walks come first, those of the last query rows and of the first keys, for an
+// even end (2 x 4096 rows, 16 heads over 4, D = 128, fp16: forward 175 us, 230 with the shortest first, backward 903 and
+// 945), and the key heads of a tile follow each other, so that with eight heads, or four, an XCD's
+// workgroups read one head's keys.
 // `even`: every walk has all its splits, which then follow each other, so that an XCD's workgroups read the same
 // part of the keys.  Else the first splits of all walks come first: some walks have fewer, and what does
 // not exist is spread over the XCDs.

