@@ -942,7 +942,11 @@ __global__ void __launch_bounds__(kThreads) k_add(Sums sums) {
         const int64_t n = j.rows * j.row, end = held.end * j.row;
         for (int64_t i = held.begin * j.row + (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < end; i += step) {
             // (as in the forward, a count that was not written is cut to the workspace)
-            const int splits = kCausal ? max(1, min(j.pieces[i / j.dim], j.splits)) : j.splits;
+            int splits = j.splits;
+            if (kCausal) {
+                const int64_t at = n >> 32 ? i / j.dim : static_cast<uint32_t>(i) / static_cast<uint32_t>(j.dim);
+                splits = max(1, min(j.pieces[at], splits));
+            }
             if (kCausal && splits == 1) continue;
             f32x8 v = load8(j.part + i);
 #pragma unroll 8

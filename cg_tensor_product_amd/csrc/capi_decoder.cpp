@@ -13,8 +13,10 @@ constexpr int64_t kMostBlocks = int64_t(1) << 24;  // a launch holds fewer than 
 oeq_status check_embedding_sizes(oeq_dtype dtype, int64_t n_table, int64_t n_cols, int64_t n_rows) {
     OEQ_TRY(check_dtype(dtype));
     if (n_table < 0 || n_cols < 0 || n_rows < 0) return fail(OEQ_ERR_INVALID_ARG, "negative size");
-    if (n_table >= kMaxRows || n_rows >= kMaxRows || n_cols >= kMaxRows)
-        return fail(OEQ_ERR_UNSUPPORTED, "table rows, rows and columns must be below 2^31 - 1");
+    if (n_table >= kMaxRows || n_rows >= kMaxRows)
+        return fail(OEQ_ERR_UNSUPPORTED, "table rows and rows must be below 2^31 - 1");
+    if (n_cols >= int64_t(1) << 23)  // the second dimension of a launch counts pieces of 256 columns, to 65535
+        return fail(OEQ_ERR_UNSUPPORTED, "columns must be below 2^23");
     if (ro::embedding_blocks(n_table, n_cols, n_rows) >= kMostBlocks)
         return fail(OEQ_ERR_UNSUPPORTED, "too many rows or columns for one launch");
     return OEQ_OK;

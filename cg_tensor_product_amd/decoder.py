@@ -106,6 +106,7 @@ def _rms_fwd(x, weight, residual, eps, out, total, out_dtype):
     code, dev = _head(x, "x")
     ld = _row_stride(x, "x")
     rows, cols = x.shape
+    out_dtype = out_dtype or x.dtype
     w = _dense(weight, (cols,), _F32, dev, "weight")
     res, ld_r, at, ld_s = None, 0, None, 0
     if residual is not None:
@@ -141,7 +142,7 @@ def oeq_rms_norm_fwd(x, weight=None, residual=None, eps: float = 1e-5, out=None,
     (fp32 [columns]).  sum is x + residual in x's type (the residual stream; x itself where there is
     no residual), rstd fp32 [rows].  `sum` may supply that tensor, x and residual themselves among
     them.  Rows may be strided."""
-    out, _, rstd, total = _rms_fwd(x, weight, residual, eps, out, sum, x.dtype)
+    out, _, rstd, total = _rms_fwd(x, weight, residual, eps, out, sum, None)
     return out, rstd, total
 
 

@@ -588,7 +588,7 @@ oeq_status oeq_cross_attn_bwd(const oeq_attn_desc *desc, const int32_t *q_ptr, c
  * so every result is bitwise repeatable. */
 
 /* Embedding lookup: out[i] = scale table[index[i]] for i < n_rows, rows of n_cols elements;
- * index is int32 or int64 (index_bytes 4 or 8).  An index outside [0, n_table) names no row:
+ * n_cols < 2^23, index is int32 or int64 (index_bytes 4 or 8).  An index outside [0, n_table) names no row:
  * it gives a row of zeros and takes no gradient (padding is index -1). */
 oeq_status oeq_embedding_fwd(oeq_dtype dtype, int64_t n_table, int64_t n_cols, int64_t n_rows,
                              const void *table, int64_t table_stride, const void *index,
@@ -596,7 +596,7 @@ oeq_status oeq_embedding_fwd(oeq_dtype dtype, int64_t n_table, int64_t n_cols, i
                              void *stream);
 
 /* Its gradient to the table: grad_table[t] = scale times the sum of grad_out[i] over the rows i
- * with index[i] = t, summed in an order that depends on the index alone and rounded once; rows
+ * with index[i] = t, summed in an order that depends on sizes and index alone and rounded once; rows
  * that no index names are zeroed.  `workspace` of oeq_embedding_workspace_size bytes. */
 oeq_status oeq_embedding_workspace_size(oeq_dtype dtype, int64_t n_table, int64_t n_cols,
                                         int64_t n_rows, size_t *bwd_bytes);

@@ -27,7 +27,7 @@ def _emb_bwd(dtype=0, table=50, cols=8, rows=4, index=A, size=8, scale=1.0, go=A
 
 SHARED = [
     (dict(dtype=1), 2), (dict(dtype=9), 2), (dict(table=-1), 1), (dict(cols=-1), 1), (dict(rows=-1), 1),
-    (dict(table=2**31 - 1), 2), (dict(rows=2**31 - 1), 2), (dict(cols=2**31 - 1), 2), (dict(size=2), 1), (dict(size=0), 1),
+    (dict(table=2**31 - 1), 2), (dict(rows=2**31 - 1), 2), (dict(cols=2**31 - 1), 2), (dict(cols=2**23), 2), (dict(size=2), 1), (dict(size=0), 1),
     (dict(index=None), 1), (dict(index=P(4100)), 1), (dict(index=P(4098), size=4), 1), (dict(scale=float("nan")), 1),
     (dict(scale=float("inf")), 1), (dict(scale=1e300), 1),
 ]
