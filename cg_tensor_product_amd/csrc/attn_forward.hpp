@@ -9,7 +9,7 @@
 // operand is read transposed from it.
 //
 // Two ways to split the work (kSplitKeys):
-//   false: the four waves own 32 query rows each and share tiles of 64 keys;
+//   false: the four waves own 32 query rows each and share tiles of 64 keys (causal fp32 of 32);
 //   true:  for few query rows (single tokens, small structures) the four waves share 32 rows
 //          and take tiles of 32 keys in turn, each through LDS of its own and without
 //          barriers; their results are joined in LDS at the end.
@@ -41,9 +41,12 @@ constexpr int kWaves = 4;
 // tiles scale nothing (a device known from published attention kernels).
 constexpr float kLag = 8.f;
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kCausal>
 struct Tiles {
-    static constexpr int kKeys = kSplitKeys ? 32 : 64;
+    // Causal fp32 above 32 columns: half a tile that the limit cuts off is not multiplied, which pays for the
+    // barriers (64 sequences of up to 200 rows, 8 heads of 64: 53 -> 46 us, of 128 95 -> 88, 32 x 400 rows of 96 211 ->
+    // 181; 16 x 800 rows of 128 338 -> 347, and at D = 32 16 x 800 rows 95 -> 102).
+    static constexpr int kKeys = kSplitKeys || (kCausal && sizeof(T) == 4 && kDim > 32) ? 32 : 64;
     static constexpr int kRow = kTileRow<T, kDim>;
     static constexpr int kRows = kSplitKeys ? 32 : 128;  // query rows of a workgroup
     static constexpr int kStage = kSplitKeys ? 64 : kThreads;
@@ -115,7 +118,7 @@ __device__ __forceinline__ float sum_of(f32x16 v) {
 template <class T, int kDim, bool kDrop, bool kSplitKeys, bool kCausal>
 __global__ void __launch_bounds__(kThreads, (kCausal ? kHeld<T, kDim> : 1))
     k_forward(AttnArgs a, int splits, int64_t slots, Partial partial) {
-    using C = Tiles<T, kDim, kSplitKeys>;
+    using C = Tiles<T, kDim, kSplitKeys, kCausal>;
     constexpr int kKeys = C::kKeys, kRow = C::kRow, kSteps = kDim / 16, kOut = kDim / 32, kSub = kKeys / 32;
     __shared__ __attribute__((aligned(16))) char lds[C::kBytes];
     const Place w = place_of<C::kRows, kCausal>(a, blockIdx.x, true, splits, slots, partial.piece == 0);

@@ -13,14 +13,14 @@ namespace readout {
 
 namespace {
 
-Choice choose(const AttnArgs &a) {
+Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     Choice c{};
     const int64_t rows = a.q_rows * a.share;
     // Sharing keys among the waves was slower from 33 rows a sequence on: 64 x 120 rows, 8 heads of 32, fp32, 25 -> 28
     // us, 256 x 60 rows 42 -> 47, D = 128 97 -> 105; only few long walks gain (16 x 800 rows: 108 -> 90).
     c.split_keys = rows <= 32 * int64_t(a.n_struct);
     c.slots = tile_slots(a.q_rows, a.n_struct, a.share, c.split_keys ? 32 : 128);
-    const int64_t base = c.slots * a.kv_heads, tile = c.split_keys ? 32 : 64;
+    const int64_t base = c.slots * a.kv_heads, tile = c.split_keys || (dtype == OEQ_F32 && a.dim > 32) ? 32 : 64;
     // Tiles of all walks, for sequences of the average lengths, and of the longest of these.  A piece is what a
     // workgroup has if the work is spread evenly over the chip, 256 keys at least; sequences of twice the
     // average length are still cut so, longer ones into longer pieces.  (8 sequences of up to 2048 rows, 8 heads over 4
@@ -44,15 +44,15 @@ Choice choose(const AttnArgs &a) {
 
 }  // namespace
 
-size_t causal_attn_fwd_workspace(oeq_dtype, const AttnArgs &a) { return forward_workspace(a, choose(a), true); }
+size_t causal_attn_fwd_workspace(oeq_dtype dtype, const AttnArgs &a) { return forward_workspace(a, choose(dtype, a), true); }
 
-int64_t causal_attn_fwd_blocks(oeq_dtype, const AttnArgs &a) { return choose(a).blocks; }
+int64_t causal_attn_fwd_blocks(oeq_dtype dtype, const AttnArgs &a) { return choose(dtype, a).blocks; }
 
 hipError_t causal_attn_fwd(oeq_dtype dtype, const AttnArgs &a, hipStream_t stream) {
     switch (dtype) {
-        case OEQ_F32: return forward<float, true>(a, choose(a), stream);
-        case OEQ_F16: return forward<f16, true>(a, choose(a), stream);
-        case OEQ_BF16: return forward<bf16, true>(a, choose(a), stream);
+        case OEQ_F32: return forward<float, true>(a, choose(dtype, a), stream);
+        case OEQ_F16: return forward<f16, true>(a, choose(dtype, a), stream);
+        case OEQ_BF16: return forward<bf16, true>(a, choose(dtype, a), stream);
         default: return hipErrorInvalidValue;
     }
 }
