@@ -33,9 +33,10 @@ inline Choice choose(const AttnArgs &a) {
     // Three workgroups a compute unit: 142 us and 7 for the sum at 512, 129 and 13 at 1024 (8 sequences of up to 2048
     // rows, as above), 130 and 10 here.
     const int64_t fill = 768;
-    c.piece = static_cast<int>(std::max<int64_t>(8, (total + fill - 1) / fill));
-    const auto splits = [&](int64_t longest) {
-        const int64_t most = longest <= c.piece ? 1 : ((a.n_struct > 1 ? 2 : 1) * longest + c.piece - 1) / c.piece;
+    const int64_t longest = std::max(m / 32, n / kRowTile) + 1;
+    c.piece = static_cast<int>(std::max<int64_t>(8, std::min((total + fill - 1) / fill, longest)));
+    const auto splits = [&](int64_t walk) {
+        const int64_t most = walk <= c.piece ? 1 : ((a.n_struct > 1 ? 2 : 1) * walk + c.piece - 1) / c.piece;
         return static_cast<int>(most > 16 ? 16 : most);
     };
     c.q_splits = splits(m / 32 + 1);

@@ -34,7 +34,7 @@ Choice choose(oeq_dtype dtype, const AttnArgs &a) {
     }
     const int64_t longest = m / tile + 1, walk = (m > n ? m - n / 2 : m / 2) / tile + 1;
     const int64_t total = (rows / (c.split_keys ? 32 : 128) + 1) * a.kv_heads * walk, fill = 256 * (a.dim <= 32 ? 3 : 2);
-    c.piece = static_cast<int>(std::max<int64_t>(256 / tile, (total + fill - 1) / fill));
+    c.piece = static_cast<int>(std::min(std::max<int64_t>(256 / tile, (total + fill - 1) / fill), longest));
     const int64_t splits = longest <= c.piece ? 1 : ((a.n_struct > 1 ? 2 : 1) * longest + c.piece - 1) / c.piece;
     c.splits = static_cast<int>(splits > 16 ? 16 : splits);
     if (c.splits == 1) c.piece = 0;

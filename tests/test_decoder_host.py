@@ -171,3 +171,18 @@ def test_causal_attn_workspace_sizes():
     empty = _desc(n_struct=0, q_rows=0, k_rows=0)
     assert size(ctypes.byref(empty), ctypes.byref(f), ctypes.byref(b)) == 0 and f.value == b.value == 0
     assert _attn(empty, q_ptr=None, k_ptr=None, q=None, k=None, v=None, out=None, lse=None) == 0
+
+
+@pytest.mark.parametrize("rows", [1 << 24, 1 << 26, (1 << 26) + 777777, (1 << 27) - 400])
+@pytest.mark.parametrize("n_struct", [1, 2, 3, 1000])
+@pytest.mark.parametrize("dtype", [0, 2, 3])
+def test_causal_attn_workspace_of_the_longest_walks(rows, n_struct, dtype):
+    # enough rows to fill the chip without cutting a walk: no partial results, however long the walks are
+    d = _desc(n_struct=n_struct, n_heads=8, n_kv_heads=8, head_dim=32, q_rows=rows, k_rows=rows, dtype=dtype)
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    status = oeq.lib().oeq_causal_attn_workspace_size(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b))
+    if 2 * 8 * (rows // 128 + n_struct) >= 1 << 24:  # the backward's workgroups, of both roles
+        assert status == 2
+        return
+    assert status == 0, _message()
+    assert f.value == 0 and rows * 8 * 4 <= b.value < rows * 8 * 4 + 4096  # delta
